@@ -128,6 +128,7 @@ def lib():
         for name in EXPORTS:
             if name not in ("mega_moe_destroy", "mega_moe_strerror"):
                 getattr(L, name).restype = i32
+        ops._bind(L)
         _lib = L
     return _lib
 
@@ -403,3 +404,8 @@ class MegaMoE:
             n *= d
         itemsize = torch.empty(0, dtype=dtype).element_size()
         return self.workspace[off:off + n * itemsize].view(dtype).view(*shape)
+
+
+# --------------------------------------------------------------- operators around the layer
+from . import ops  # noqa: E402
+from .ops import *  # noqa: E402,F401,F403

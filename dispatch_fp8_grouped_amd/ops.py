@@ -1,0 +1,178 @@
+"""Operators around the fused MoE layer (include/mega_moe_ops.h): products grouped by expert and their
+gradients.
+
+The functions with the C names marshal arguments only; the short names below them check shapes, types and
+devices, allocate what they return, and call them.  Everything runs in the HIP kernels of libmegamoe.so.
+
+    y = mm.grouped_forward(x_sorted, w, offsets)                     # y[m] = x[m] @ w[e].T
+    dx = mm.grouped_backward_rows(dy, w, offsets)
+    dw = mm.grouped_backward_weight(dy, x_sorted, offsets)
+
+Tensors must be dense, on one GPU.  Calls run on the current stream of that GPU, or on `stream` (a torch
+stream or a stream handle); a tensor that a call returns belongs to the stream of the call.  The functions
+compute values and gradients and record no autograd graph.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+BF16 = 0
+FP16 = 1
+FP32 = 2
+
+# Exported symbols of include/mega_moe_ops.h
+OPS_EXPORTS = ("mega_moe_grouped_forward", "mega_moe_grouped_backward_rows", "mega_moe_grouped_backward_weight")
+
+
+__all__ = ["BF16", "FP16", "FP32", "OPS_EXPORTS", *OPS_EXPORTS,
+           "grouped_forward", "grouped_backward_rows", "grouped_backward_weight"]
+
+
+def _bind(L):
+    """Argument types of the operators' symbols (called once, by lib())."""
+    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    rows = [vp, vp, vp, vp, i64, i32, i32, i32, i32]
+    L.mega_moe_grouped_forward.argtypes = rows + [vp, vp]
+    L.mega_moe_grouped_backward_rows.argtypes = rows + [vp, vp]
+    L.mega_moe_grouped_backward_weight.argtypes = rows + [i32, i32, vp, vp]
+    for name in OPS_EXPORTS:
+        getattr(L, name).restype = i32
+
+
+def _core():
+    import dispatch_fp8_grouped_amd as mm
+    return mm
+
+
+# --------------------------------------------------------------- the C entry points, same names
+def mega_moe_grouped_forward(x, w, offsets, y, rows, n, k, groups, dtype, device_status=None, stream=None):
+    mm = _core()
+    mm._check(mm.lib().mega_moe_grouped_forward(mm._ptr(x), mm._ptr(w), mm._ptr(offsets), mm._ptr(y), rows, n, k, groups,
+                                                dtype, mm._ptr(device_status), mm._stream(stream)),
+              "mega_moe_grouped_forward")
+
+
+def mega_moe_grouped_backward_rows(dy, w, offsets, dx, rows, n, k, groups, dtype, device_status=None, stream=None):
+    mm = _core()
+    mm._check(mm.lib().mega_moe_grouped_backward_rows(mm._ptr(dy), mm._ptr(w), mm._ptr(offsets), mm._ptr(dx), rows, n, k,
+                                                      groups, dtype, mm._ptr(device_status), mm._stream(stream)),
+              "mega_moe_grouped_backward_rows")
+
+
+def mega_moe_grouped_backward_weight(dy, x, offsets, dw, rows, n, k, groups, dtype, out_dtype, accumulate=False,
+                                     device_status=None, stream=None):
+    mm = _core()
+    mm._check(mm.lib().mega_moe_grouped_backward_weight(mm._ptr(dy), mm._ptr(x), mm._ptr(offsets), mm._ptr(dw), rows, n,
+                                                        k, groups, dtype, out_dtype, 1 if accumulate else 0,
+                                                        mm._ptr(device_status), mm._stream(stream)),
+              "mega_moe_grouped_backward_weight")
+
+
+# --------------------------------------------------------------- checks
+def _want(name, t, shape, dtypes, device=None):
+    """t is a dense GPU tensor of this shape and one of these types (shape None: any)."""
+    ok = t is not None and t.device.type == "cuda" and t.is_contiguous() and t.dtype in dtypes
+    ok = ok and (shape is None or tuple(t.shape) == tuple(shape)) and (device is None or t.device == device)
+    if not ok:
+        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}" + (
+            "" if t.is_contiguous() else ", not contiguous")
+        types = " or ".join(str(d) for d in dtypes)
+        raise ValueError(f"{name}: want contiguous cuda {types}{'' if shape is None else ' ' + str(tuple(shape))}"
+                         f"{'' if device is None else ' on ' + str(device)}, got {got}")
+
+
+class _Call:
+    """Makes `device` and the call's stream current, so that allocations belong to that stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.ctx = None
+        if stream is None:
+            if torch.cuda.current_device() != device.index:
+                self.ctx = torch.cuda.device(device)
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device} for tensors on {device}")
+            self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _halves():
+    import torch
+    return {torch.bfloat16: BF16, torch.float16: FP16}
+
+
+def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream, call):
+    import torch
+    kinds = _halves()
+    _want("w", w, None, kinds)
+    if w.dim() != 3 or rows_in is None or rows_in.dim() != 2:
+        raise ValueError(f"{what}: want w [groups, n, k] and rows of two dimensions")
+    groups, n, k = w.shape
+    inner, outer = (k, n) if contract_k else (n, k)
+    rows = rows_in.shape[0]
+    _want("x" if contract_k else "dy", rows_in, (rows, inner), (w.dtype,), w.device)
+    _want("offsets", offsets, (groups + 1,), (torch.int32,), w.device)
+    if status is not None:
+        _want("status", status, (1,), (torch.int32,), w.device)
+    with _Call(w.device, stream):
+        if out is None:
+            out = torch.empty((rows, outer), dtype=w.dtype, device=w.device)
+        else:
+            _want("out", out, (rows, outer), (w.dtype,), w.device)
+        call(rows_in, w, offsets, out, rows, n, k, groups, kinds[w.dtype], status)
+    return out
+
+
+def grouped_forward(x, w, offsets, out=None, status=None, stream=None):
+    """y[m] = x[m] @ w[e].T for the rows m of group e, offsets[e] .. offsets[e+1]-1.
+
+    x [rows, k], w [groups, n, k], both bfloat16 or float16; offsets int32 [groups + 1].  Rows that belong
+    to no group are not written (in a new `out` they hold what the allocation held).  status: int32 [1], or
+    None; see mega_moe_ops.h."""
+    return _grouped("grouped_forward", x, w, offsets, True, out, status, stream, mega_moe_grouped_forward)
+
+
+def grouped_backward_rows(dy, w, offsets, out=None, status=None, stream=None):
+    """dx[m] = dy[m] @ w[e]: the gradient of grouped_forward's rows.  dy [rows, n] -> dx [rows, k]."""
+    return _grouped("grouped_backward_rows", dy, w, offsets, False, out, status, stream, mega_moe_grouped_backward_rows)
+
+
+def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=False, status=None, stream=None):
+    """dw[e] = dy_e.T @ x_e: the gradient of grouped_forward's weights, [groups, n, k] in `dtype` (the
+    operands', or float32).  A group without rows gets zeros.  With accumulate, `out` (float32) is added to."""
+    import torch
+    kinds = _halves()
+    _want("x", x, None, kinds)
+    if x.dim() != 2 or dy is None or dy.dim() != 2 or offsets is None or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("grouped_backward_weight: want dy [rows, n], x [rows, k] and offsets [groups + 1]")
+    rows, k = x.shape
+    n, groups = dy.shape[1], offsets.numel() - 1
+    _want("dy", dy, (rows, n), (x.dtype,), x.device)
+    _want("offsets", offsets, (groups + 1,), (torch.int32,), x.device)
+    if dtype is None:
+        dtype = out.dtype if out is not None else x.dtype
+    if dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"dtype: want {x.dtype} or torch.float32, got {dtype}")
+    if accumulate and (out is None or dtype != torch.float32):
+        raise ValueError("accumulate needs a float32 `out`")
+    if status is not None:
+        _want("status", status, (1,), (torch.int32,), x.device)
+    with _Call(x.device, stream):
+        if out is None:
+            out = torch.empty((groups, n, k), dtype=dtype, device=x.device)
+        else:
+            _want("out", out, (groups, n, k), (dtype,), x.device)
+        mega_moe_grouped_backward_weight(dy, x, offsets, out, rows, n, k, groups, kinds[x.dtype],
+                                         FP32 if dtype == torch.float32 else kinds[dtype], accumulate, status)
+    return out
