@@ -1,9 +1,11 @@
 """Operators around the fused MoE layer (include/mega_moe_ops.h): products grouped by expert and their
-gradients.
+gradients, the router with its gradient and the ordering of its pairs.
 
 The functions with the C names marshal arguments only; the short names below them check shapes, types and
 devices, allocate what they return, and call them.  Everything runs in the HIP kernels of libmegamoe.so.
 
+    idx, weights = mm.router_topk(logits, 8, bias=bias, score="sigmoid", num_groups=8, topk_groups=4, group_top=2)
+    offsets, order, slot = mm.group_by_expert(idx, num_experts)      # rows sorted by expert
     y = mm.grouped_forward(x_sorted, w, offsets)                     # y[m] = x[m] @ w[e].T
     dx = mm.grouped_backward_rows(dy, w, offsets)
     dw = mm.grouped_backward_weight(dy, x_sorted, offsets)
@@ -20,22 +22,40 @@ from typing import Optional
 BF16 = 0
 FP16 = 1
 FP32 = 2
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 
 # Exported symbols of include/mega_moe_ops.h
-OPS_EXPORTS = ("mega_moe_grouped_forward", "mega_moe_grouped_backward_rows", "mega_moe_grouped_backward_weight")
+OPS_EXPORTS = ("mega_moe_grouped_forward", "mega_moe_grouped_backward_rows", "mega_moe_grouped_backward_weight",
+               "mega_moe_router_topk", "mega_moe_router_backward", "mega_moe_group_workspace_bytes",
+               "mega_moe_group_by_expert")
 
 
-__all__ = ["BF16", "FP16", "FP32", "OPS_EXPORTS", *OPS_EXPORTS,
-           "grouped_forward", "grouped_backward_rows", "grouped_backward_weight"]
+__all__ = ["BF16", "FP16", "FP32", "SCORE_SOFTMAX", "SCORE_SIGMOID", "OPS_EXPORTS", *OPS_EXPORTS,
+           "grouped_forward", "grouped_backward_rows", "grouped_backward_weight", "mega_moe_router_config",
+           "router_topk", "router_backward", "group_by_expert"]
+
+
+class mega_moe_router_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
 
 
 def _bind(L):
     """Argument types of the operators' symbols (called once, by lib())."""
-    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    vp, i32, i64, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
     rows = [vp, vp, vp, vp, i64, i32, i32, i32, i32]
     L.mega_moe_grouped_forward.argtypes = rows + [vp, vp]
     L.mega_moe_grouped_backward_rows.argtypes = rows + [vp, vp]
     L.mega_moe_grouped_backward_weight.argtypes = rows + [i32, i32, vp, vp]
+    cfg = ctypes.POINTER(mega_moe_router_config)
+    L.mega_moe_router_topk.argtypes = [cfg, vp, vp, vp, vp, vp]
+    L.mega_moe_router_backward.argtypes = [cfg, vp, vp, vp, vp, vp]
+    L.mega_moe_group_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(u64)]
+    L.mega_moe_group_by_expert.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, u64, vp]
     for name in OPS_EXPORTS:
         getattr(L, name).restype = i32
 
@@ -67,6 +87,35 @@ def mega_moe_grouped_backward_weight(dy, x, offsets, dw, rows, n, k, groups, dty
                                                         k, groups, dtype, out_dtype, 1 if accumulate else 0,
                                                         mm._ptr(device_status), mm._stream(stream)),
               "mega_moe_grouped_backward_weight")
+
+
+def mega_moe_router_topk(cfg: mega_moe_router_config, logits, bias, topk_idx, topk_weights, stream=None):
+    mm = _core()
+    mm._check(mm.lib().mega_moe_router_topk(ctypes.byref(cfg), mm._ptr(logits), mm._ptr(bias), mm._ptr(topk_idx),
+                                            mm._ptr(topk_weights), mm._stream(stream)), "mega_moe_router_topk")
+
+
+def mega_moe_router_backward(cfg: mega_moe_router_config, dweights, logits, topk_idx, dlogits, stream=None):
+    mm = _core()
+    mm._check(mm.lib().mega_moe_router_backward(ctypes.byref(cfg), mm._ptr(dweights), mm._ptr(logits), mm._ptr(topk_idx),
+                                                mm._ptr(dlogits), mm._stream(stream)), "mega_moe_router_backward")
+
+
+def mega_moe_group_workspace_bytes(pairs: int, num_local_experts: int) -> int:
+    mm = _core()
+    out = ctypes.c_uint64(0)
+    mm._check(mm.lib().mega_moe_group_workspace_bytes(pairs, num_local_experts, ctypes.byref(out)),
+              "mega_moe_group_workspace_bytes")
+    return out.value
+
+
+def mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, offsets, order, slot, workspace,
+                             workspace_bytes=None, stream=None):
+    mm = _core()
+    nbytes = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
+    mm._check(mm.lib().mega_moe_group_by_expert(mm._ptr(topk_idx), pairs, first_expert, num_local_experts,
+                                                mm._ptr(offsets), mm._ptr(order), mm._ptr(slot), mm._ptr(workspace),
+                                                nbytes, mm._stream(stream)), "mega_moe_group_by_expert")
 
 
 # --------------------------------------------------------------- checks
@@ -176,3 +225,68 @@ def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=Fal
         mega_moe_grouped_backward_weight(dy, x, offsets, out, rows, n, k, groups, kinds[x.dtype],
                                          FP32 if dtype == torch.float32 else kinds[dtype], accumulate, status)
     return out
+
+
+def _router_config(logits, topk, score, num_groups, topk_groups, group_top, renormalize, scale):
+    import torch
+    _want("logits", logits, None, (torch.float32, *_halves()))
+    if logits.dim() < 2 or logits.shape[-1] < 1:
+        raise ValueError(f"logits: want [..., num_experts], got {tuple(logits.shape)}")
+    if score not in _SCORES:
+        raise ValueError(f"score: want one of {sorted(_SCORES)}, got {score!r}")
+    experts = logits.shape[-1]
+    kind = FP32 if logits.dtype == torch.float32 else _halves()[logits.dtype]
+    return mega_moe_router_config(logits.numel() // experts, experts, topk, _SCORES[score], num_groups, topk_groups,
+                                  group_top, 1 if renormalize else 0, scale, kind)
+
+
+def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_groups=1, group_top=1, renormalize=True,
+                scale=1.0, stream=None):
+    """The `topk` experts of every token and their weights, (topk_idx int64, topk_weights float32) of shape
+    [..., topk], as MegaMoE.forward takes them.
+
+    logits [..., num_experts] (float32, bfloat16 or float16); -inf or NaN masks an expert.  bias: float32
+    [num_experts], added to the scores for the choice only.  Only experts of the topk_groups best of num_groups
+    equal groups are eligible; a group is worth the sum of its group_top (1 or 2) best.  See mega_moe_ops.h."""
+    import torch
+    cfg = _router_config(logits, topk, score, num_groups, topk_groups, group_top, renormalize, scale)
+    if bias is not None:
+        _want("bias", bias, (cfg.num_experts,), (torch.float32,), logits.device)
+    shape = (*logits.shape[:-1], max(topk, 0))
+    with _Call(logits.device, stream):
+        idx = torch.empty(shape, dtype=torch.int64, device=logits.device)
+        weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+        mega_moe_router_topk(cfg, logits, bias, idx, weights)
+    return idx, weights
+
+
+def router_backward(dweights, logits, topk_idx, score="softmax", renormalize=True, scale=1.0, stream=None):
+    """dlogits (of the logits' type) from the gradient of router_topk's weights, the choice held fixed."""
+    import torch
+    if topk_idx is None or topk_idx.dim() < 2:
+        raise ValueError("topk_idx: want [..., topk]")
+    topk = topk_idx.shape[-1]
+    cfg = _router_config(logits, topk, score, 1, 1, 1, renormalize, scale)
+    _want("topk_idx", topk_idx, (*logits.shape[:-1], topk), (torch.int64,), logits.device)
+    _want("dweights", dweights, (*logits.shape[:-1], topk), (torch.float32,), logits.device)
+    with _Call(logits.device, stream):
+        dlogits = torch.empty_like(logits)
+        mega_moe_router_backward(cfg, dweights, logits, topk_idx, dlogits)
+    return dlogits
+
+
+def group_by_expert(topk_idx, num_local_experts, first_expert=0, stream=None):
+    """Sort the chosen pairs by expert: (offsets int32 [num_local_experts + 1], order int32 [pairs], slot int32 of
+    topk_idx's shape).  order[i] is the flat pair t*topk + k at place i (-1 behind the last), slot its inverse
+    (-1 for a pair of no local expert).  Row i of the grouped products is then token order[i] // topk."""
+    import torch
+    _want("topk_idx", topk_idx, None, (torch.int64,))
+    pairs, device = topk_idx.numel(), topk_idx.device
+    nbytes = mega_moe_group_workspace_bytes(pairs, num_local_experts)
+    with _Call(device, stream):
+        offsets = torch.empty(num_local_experts + 1, dtype=torch.int32, device=device)
+        order = torch.empty(pairs, dtype=torch.int32, device=device)
+        slot = torch.empty(topk_idx.shape, dtype=torch.int32, device=device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, offsets, order, slot, workspace)
+    return offsets, order, slot

@@ -1,6 +1,9 @@
 /*
  * mega_moe_ops.h -- operators around the fused MoE layer of mega_moe.h, for one GPU (MI355X, gfx950):
- *   - products grouped by expert with ragged row counts, and their gradients (training the experts).
+ *   - products grouped by expert with ragged row counts, and their gradients (training the experts);
+ *   - the router: choosing and weighing the experts of every token (topk_idx / topk_weights as
+ *     mega_moe_forward takes them), its gradient, and the ordering of the chosen pairs by expert that
+ *     the grouped products read.
  *
  * Conventions are those of mega_moe.h: 0 or a negative MEGA_MOE_ERR_* code, nothing throws; device
  * pointers (16-byte aligned unless the comment says otherwise), dense row-major tensors; work is enqueued
@@ -61,6 +64,66 @@ int32_t mega_moe_grouped_backward_weight(const void* dy, const void* x, const in
                                          int64_t rows, int32_t n, int32_t k, int32_t groups, int32_t dtype,
                                          int32_t out_dtype, int32_t accumulate, uint32_t* device_status,
                                          void* stream);
+
+/* ------------------------------------------------------------------ router */
+#define MEGA_MOE_SCORE_SOFTMAX 0   /* s = softmax of the token's logits over all its unmasked experts */
+#define MEGA_MOE_SCORE_SIGMOID 1   /* s = 1 / (1 + exp(-logit))                                       */
+
+typedef struct mega_moe_router_config {
+    int64_t tokens;        /* T: 0 .. 2^31-1; T * topk < 2^31                                          */
+    int32_t num_experts;   /* E: 1 .. MEGA_MOE_MAX_EXPERTS                                             */
+    int32_t topk;          /* K: 1 .. min(E, MEGA_MOE_MAX_TOPK)                                        */
+    int32_t score;         /* MEGA_MOE_SCORE_*                                                         */
+    int32_t num_groups;    /* experts in equal consecutive groups; divides E; 1 .. 64                  */
+    int32_t topk_groups;   /* groups a token may choose from, 1 .. num_groups                          */
+    int32_t group_top;     /* a group is worth the sum of its group_top best experts: 1 or 2           */
+    int32_t renormalize;   /* nonzero: the chosen scores are divided by their sum                      */
+    float scale;           /* factor of every weight, finite                                           */
+    int32_t dtype;         /* of logits (and dlogits): MEGA_MOE_BF16, _FP16 or _FP32                   */
+} mega_moe_router_config;
+
+/* For every token: the K experts that rank highest, and their weights.
+ *   logits        dtype [T][E].  -inf or NaN masks an expert of that token: it scores 0 and is never
+ *                 chosen.  +inf counts as the largest fp32 number.
+ *   bias          float [E] or NULL: added to the scores for the choice only, not in the weights.  An
+ *                 expert whose biased score is -inf or NaN is not chosen.
+ *   topk_idx      int64 [T][K]: expert ids, highest rank first; equal ranks: the lower id first.  A token
+ *                 with fewer than K experts to choose from gets -1 (no expert) in the places left.
+ *   topk_weights  float [T][K]: scale * s, or scale * s / (sum of the chosen s) when renormalizing; 0 where
+ *                 topk_idx is -1, and all 0 where the sum is 0 (sigmoid scores of logits below -700; in
+ *                 the renormalized softmax the experts that were not chosen cancel out, and it is not)
+ * Rank: s + bias; without a bias the logit itself, whose order is that of s.  With num_groups > 1 only
+ * experts of the topk_groups best groups are eligible; a group's worth is the sum of its group_top
+ * highest ranks over unmasked experts (without a bias and with group_top 2: of their s), equal worths: the lower
+ * group.  Scores and ranks are computed in fp64, so that a choice between close scores does not hang on
+ * fp32 rounding.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP. */
+int32_t mega_moe_router_topk(const mega_moe_router_config* cfg, const void* logits, const float* bias,
+                             int64_t* topk_idx, float* topk_weights, void* stream);
+
+/* Gradient of the weights with respect to the logits, with the choice held fixed (a bias gets none).
+ *   dweights  float [T][K], topk_idx int64 [T][K] as the forward pass returned it (entries outside
+ *             0 .. E-1 are ignored; an expert named twice counts twice), logits as in the forward pass
+ *   dlogits   dtype [T][E]: every entry written; 0 for masked experts
+ * The scores are computed again from the logits.  num_groups, topk_groups and group_top are not used.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP. */
+int32_t mega_moe_router_backward(const mega_moe_router_config* cfg, const float* dweights, const void* logits,
+                                 const int64_t* topk_idx, void* dlogits, void* stream);
+
+/* Order chosen pairs by expert, for the grouped products: pair p = t*K + k goes to expert topk_idx[p].
+ *   topk_idx   int64 [pairs]; entries outside first_expert .. first_expert + num_local_experts - 1
+ *              belong to no group here
+ *   offsets    int32 [num_local_experts + 1]: first place of every local expert's pairs, and their number
+ *   order      int32 [pairs]: order[i] = pair at place i; pairs of one expert in increasing order; -1 from
+ *              offsets[num_local_experts] on
+ *   slot       int32 [pairs]: the place of pair p, -1 if it belongs to no group here
+ *   workspace  mega_moe_group_workspace_bytes() bytes; its contents do not matter
+ * pairs 0 .. 2^31-1 (pointers of pair arrays may be NULL at 0); num_local_experts 1 .. MEGA_MOE_MAX_EXPERTS.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP. */
+int32_t mega_moe_group_workspace_bytes(int64_t pairs, int32_t num_local_experts, uint64_t* bytes_out /* host */);
+int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t first_expert,
+                                 int32_t num_local_experts, int32_t* offsets, int32_t* order, int32_t* slot,
+                                 void* workspace, uint64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -56,3 +56,64 @@ def test_python_checks_refuse_before_the_library():
                  lambda: mm.grouped_backward_weight(x.bfloat16(), x.bfloat16(), off)):
         with pytest.raises(ValueError):
             call()
+
+
+def router_cfg(**kw):
+    base = dict(tokens=4, num_experts=16, topk=2, score=0, num_groups=4, topk_groups=2, group_top=2, renormalize=1,
+                scale=1.0, dtype=mm.FP32)
+    base.update(kw)
+    return mm.mega_moe_router_config(*[base[n] for n, _ in mm.mega_moe_router_config._fields_])
+
+
+def test_router_refusals():
+    lib = mm.lib()
+    for kw in (dict(num_experts=0), dict(num_experts=4097), dict(topk=0), dict(topk=17), dict(topk=65, num_experts=256),
+               dict(score=2), dict(num_groups=0), dict(num_groups=3), dict(num_groups=128, num_experts=256),
+               dict(topk_groups=0), dict(topk_groups=5), dict(group_top=0), dict(group_top=3), dict(dtype=3),
+               dict(scale=float("inf")), dict(scale=float("nan")), dict(tokens=1 << 31), dict(tokens=1 << 30, topk=4)):
+        c = router_cfg(**kw)
+        assert lib.mega_moe_router_topk(ctypes.byref(c), P, P, P, P, None) == mm.ERR_UNSUPPORTED, kw
+        assert lib.mega_moe_router_backward(ctypes.byref(c), P, P, P, P, None) == mm.ERR_UNSUPPORTED, kw
+    c = router_cfg()
+    assert lib.mega_moe_router_topk(None, P, P, P, P, None) == mm.ERR_INVALID_ARG
+    assert lib.mega_moe_router_backward(None, P, P, P, P, None) == mm.ERR_INVALID_ARG
+    neg = router_cfg(tokens=-1)
+    assert lib.mega_moe_router_topk(ctypes.byref(neg), P, P, P, P, None) == mm.ERR_INVALID_ARG
+    for i in (0, 1, 2, 3):
+        args = [P, P, P, P]
+        args[i] = ODD
+        assert lib.mega_moe_router_topk(ctypes.byref(c), *args, None) == mm.ERR_INVALID_ARG, i
+        assert lib.mega_moe_router_backward(ctypes.byref(c), *args, None) == mm.ERR_INVALID_ARG, i
+        args[i] = None
+        if i != 1:                                     # the bias may be missing
+            assert lib.mega_moe_router_topk(ctypes.byref(c), *args, None) == mm.ERR_INVALID_ARG, i
+        assert lib.mega_moe_router_backward(ctypes.byref(c), *args, None) == mm.ERR_INVALID_ARG, i
+    none = router_cfg(tokens=0)
+    assert lib.mega_moe_router_topk(ctypes.byref(none), None, None, None, None, None) == mm.OK
+    assert lib.mega_moe_router_backward(ctypes.byref(none), None, None, None, None, None) == mm.OK
+
+
+def test_ordering_refusals():
+    lib = mm.lib()
+    out = ctypes.c_uint64(0)
+    assert lib.mega_moe_group_workspace_bytes(10, 4, None) == mm.ERR_INVALID_ARG
+    assert lib.mega_moe_group_workspace_bytes(-1, 4, ctypes.byref(out)) == mm.ERR_INVALID_ARG
+    for pairs, experts in ((1 << 31, 4), (10, 0), (10, 4097)):
+        assert lib.mega_moe_group_workspace_bytes(pairs, experts, ctypes.byref(out)) == mm.ERR_UNSUPPORTED
+        assert lib.mega_moe_group_by_expert(P, pairs, 0, experts, P, P, P, P, 1 << 40, None) == mm.ERR_UNSUPPORTED
+    need = mm.mega_moe_group_workspace_bytes(100000, 256)
+    assert lib.mega_moe_group_by_expert(P, 100000, 0, 256, P, P, P, P, need - 1, None) == mm.ERR_WORKSPACE_TOO_SMALL
+    assert lib.mega_moe_group_by_expert(P, 10, -1, 4, P, P, P, P, need, None) == mm.ERR_INVALID_ARG
+    for i in range(5):
+        args = [P] * 5
+        args[i] = ODD
+        a = (args[0], 10, 0, 4, *args[1:])
+        assert lib.mega_moe_group_by_expert(*a, need, None) == mm.ERR_INVALID_ARG, i
+
+
+def test_router_python_checks():
+    x = torch.zeros(4, 16)
+    for call in (lambda: mm.router_topk(x, 2), lambda: mm.router_topk(None, 2), lambda: mm.group_by_expert(x.long(), 4),
+                 lambda: mm.router_backward(x[:, :2], x, x[:, :2].long()), lambda: mm.router_backward(x, x, None)):
+        with pytest.raises(ValueError):
+            call()
