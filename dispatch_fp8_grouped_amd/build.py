@@ -27,7 +27,7 @@ COMMON = [
     "-mllvm", "-disable-promote-alloca-to-lds",
 ]
 SOURCES = ["route.hip", "fill.hip", "gemm.hip", "combine.hip", "pack.hip", "host.hip",
-           "grouped.hip", "router.hip"]
+           "grouped.hip", "router.hip", "adapter.hip"]
 
 
 def _check_resources(src: str, remarks: str) -> None:

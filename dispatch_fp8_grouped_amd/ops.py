@@ -1,5 +1,5 @@
 """Operators around the fused MoE layer (include/mega_moe_ops.h): products grouped by expert and their
-gradients, the router with its gradient and the ordering of its pairs.
+gradients, the router with its gradient and the ordering of its pairs, and adapter projections.
 
 The functions with the C names marshal arguments only; the short names below them check shapes, types and
 devices, allocate what they return, and call them.  Everything runs in the HIP kernels of libmegamoe.so.
@@ -9,6 +9,7 @@ devices, allocate what they return, and call them.  Everything runs in the HIP k
     y = mm.grouped_forward(x_sorted, w, offsets)                     # y[m] = x[m] @ w[e].T
     dx = mm.grouped_backward_rows(dy, w, offsets)
     dw = mm.grouped_backward_weight(dy, x_sorted, offsets)
+    y = mm.adapter_forward(x, w, a, b, scales, offsets, adapter)     # one low-rank adapter per request
 
 Tensors must be dense, on one GPU.  Calls run on the current stream of that GPU, or on `stream` (a torch
 stream or a stream handle); a tensor that a call returns belongs to the stream of the call.  The functions
@@ -29,12 +30,12 @@ _SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 # Exported symbols of include/mega_moe_ops.h
 OPS_EXPORTS = ("mega_moe_grouped_forward", "mega_moe_grouped_backward_rows", "mega_moe_grouped_backward_weight",
                "mega_moe_router_topk", "mega_moe_router_backward", "mega_moe_group_workspace_bytes",
-               "mega_moe_group_by_expert")
+               "mega_moe_group_by_expert", "mega_moe_adapter_workspace_bytes", "mega_moe_adapter_forward")
 
 
 __all__ = ["BF16", "FP16", "FP32", "SCORE_SOFTMAX", "SCORE_SIGMOID", "OPS_EXPORTS", *OPS_EXPORTS,
            "grouped_forward", "grouped_backward_rows", "grouped_backward_weight", "mega_moe_router_config",
-           "router_topk", "router_backward", "group_by_expert"]
+           "router_topk", "router_backward", "group_by_expert", "adapter_forward"]
 
 
 class mega_moe_router_config(ctypes.Structure):
@@ -56,6 +57,8 @@ def _bind(L):
     L.mega_moe_router_backward.argtypes = [cfg, vp, vp, vp, vp, vp]
     L.mega_moe_group_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(u64)]
     L.mega_moe_group_by_expert.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, u64, vp]
+    L.mega_moe_adapter_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(u64)]
+    L.mega_moe_adapter_forward.argtypes = [vp] * 8 + [i64] + [i32] * 6 + [vp, u64, vp, vp]
     for name in OPS_EXPORTS:
         getattr(L, name).restype = i32
 
@@ -116,6 +119,23 @@ def mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, o
     mm._check(mm.lib().mega_moe_group_by_expert(mm._ptr(topk_idx), pairs, first_expert, num_local_experts,
                                                 mm._ptr(offsets), mm._ptr(order), mm._ptr(slot), mm._ptr(workspace),
                                                 nbytes, mm._stream(stream)), "mega_moe_group_by_expert")
+
+
+def mega_moe_adapter_workspace_bytes(rows: int, rank: int) -> int:
+    mm = _core()
+    out = ctypes.c_uint64(0)
+    mm._check(mm.lib().mega_moe_adapter_workspace_bytes(rows, rank, ctypes.byref(out)), "mega_moe_adapter_workspace_bytes")
+    return out.value
+
+
+def mega_moe_adapter_forward(x, w, a, b, scales, offsets, adapter, y, rows, n, k, rank, requests, adapters, dtype,
+                             workspace, workspace_bytes=None, device_status=None, stream=None):
+    mm = _core()
+    nbytes = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
+    mm._check(mm.lib().mega_moe_adapter_forward(mm._ptr(x), mm._ptr(w), mm._ptr(a), mm._ptr(b), mm._ptr(scales),
+                                                mm._ptr(offsets), mm._ptr(adapter), mm._ptr(y), rows, n, k, rank,
+                                                requests, adapters, dtype, mm._ptr(workspace), nbytes,
+                                                mm._ptr(device_status), mm._stream(stream)), "mega_moe_adapter_forward")
 
 
 # --------------------------------------------------------------- checks
@@ -290,3 +310,39 @@ def group_by_expert(topk_idx, num_local_experts, first_expert=0, stream=None):
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, offsets, order, slot, workspace)
     return offsets, order, slot
+
+
+def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=None, status=None, stream=None):
+    """y[m] = x[m] @ w.T + scales[i] * (x[m] @ a[i].T) @ b[i].T with i = adapter[r] of the request r that owns row m.
+
+    x [rows, k], w [n, k], a [adapters, rank, k], b [adapters, n, rank], all bfloat16 or float16; scales float32
+    [adapters]; offsets int32 [requests + 1] (request r owns rows offsets[r] .. offsets[r+1]-1), adapter int32
+    [requests], -1 for a request without one.  workspace: uint8 of mega_moe_adapter_workspace_bytes(), or None."""
+    import torch
+    kinds = _halves()
+    _want("w", w, None, kinds)
+    if w.dim() != 2 or x is None or x.dim() != 2 or a is None or a.dim() != 3 or adapter is None or adapter.dim() != 1:
+        raise ValueError("adapter_forward: want x [rows, k], w [n, k], a [adapters, rank, k], adapter [requests]")
+    n, k = w.shape
+    rows, adapters, rank, requests = x.shape[0], a.shape[0], a.shape[1], adapter.shape[0]
+    for name, t, shape, types in (("x", x, (rows, k), (w.dtype,)), ("a", a, (adapters, rank, k), (w.dtype,)),
+                                  ("b", b, (adapters, n, rank), (w.dtype,)),
+                                  ("scales", scales, (adapters,), (torch.float32,)),
+                                  ("offsets", offsets, (requests + 1,), (torch.int32,)),
+                                  ("adapter", adapter, (requests,), (torch.int32,))):
+        _want(name, t, shape, types, w.device)
+    if status is not None:
+        _want("status", status, (1,), (torch.int32,), w.device)
+    nbytes = mega_moe_adapter_workspace_bytes(rows, rank)
+    with _Call(w.device, stream):
+        if out is None:
+            out = torch.empty((rows, n), dtype=w.dtype, device=w.device)
+        else:
+            _want("out", out, (rows, n), (w.dtype,), w.device)
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
+        else:
+            _want("workspace", workspace, None, (torch.uint8,), w.device)
+        mega_moe_adapter_forward(x, w, a, b, scales, offsets, adapter, out, rows, n, k, rank, requests, adapters,
+                                 kinds[w.dtype], workspace, None, status)
+    return out

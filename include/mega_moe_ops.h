@@ -3,7 +3,8 @@
  *   - products grouped by expert with ragged row counts, and their gradients (training the experts);
  *   - the router: choosing and weighing the experts of every token (topk_idx / topk_weights as
  *     mega_moe_forward takes them), its gradient, and the ordering of the chosen pairs by expert that
- *     the grouped products read.
+ *     the grouped products read;
+ *   - a projection shared by many requests that each bring a low-rank adapter.
  *
  * Conventions are those of mega_moe.h: 0 or a negative MEGA_MOE_ERR_* code, nothing throws; device
  * pointers (16-byte aligned unless the comment says otherwise), dense row-major tensors; work is enqueued
@@ -30,8 +31,9 @@ extern "C" {
 #define MEGA_MOE_FP16 1
 #define MEGA_MOE_FP32 2
 
-#define MEGA_MOE_MAX_GROUP_ROWS (1 << 26)   /* rows of a grouped product */
+#define MEGA_MOE_MAX_GROUP_ROWS (1 << 26)   /* rows of a grouped product or an adapter projection */
 #define MEGA_MOE_MAX_GROUP_COLS 65536       /* its n and k */
+#define MEGA_MOE_MAX_REQUESTS 4096          /* requests of an adapter projection */
 
 /* ------------------------------------------------------------------ products grouped by expert
  * Rows are sorted by group: group e owns rows offsets[e] .. offsets[e+1]-1 of the row tensors (any count,
@@ -124,6 +126,28 @@ int32_t mega_moe_group_workspace_bytes(int64_t pairs, int32_t num_local_experts,
 int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t first_expert,
                                  int32_t num_local_experts, int32_t* offsets, int32_t* order, int32_t* slot,
                                  void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ low-rank adapters
+ * One projection for the rows of many requests, each with an adapter of its own (or none):
+ *   y[m] = x[m] w^T + scales[a] * (x[m] a_a^T) b_a^T,   a = adapter[r] of the request r that owns row m
+ *   x        dtype [rows][k], w dtype [n][k], y dtype [rows][n]
+ *   a        dtype [adapters][rank][k], b dtype [adapters][n][rank], scales float [adapters]
+ *   offsets  int32 [requests + 1] as for the grouped products: request r owns rows offsets[r] ..
+ *            offsets[r+1]-1.  Rows that belong to no request get the shared projection alone.
+ *   adapter  int32 [requests]: -1 for none; several requests may name the same adapter.  An entry outside
+ *            -1 .. adapters-1 counts as none and latches MEGA_MOE_STATUS_BAD_EXPERT_ID
+ *   rank     a multiple of 8, 8 .. 256 (adapters of lower rank are padded with zeros)
+ *   requests 0 .. MEGA_MOE_MAX_REQUESTS; adapters 1 .. 65536; rows, n, k, dtype as above
+ *   workspace mega_moe_adapter_workspace_bytes() bytes; its contents do not matter
+ * The shared sum, x a^T and the adapter's sum are held in fp32; scales[a] * x a^T enters the second product as
+ * the sum of two 16-bit numbers, the value rounded and the rounded remainder.  In fp16 it has fp16's range:
+ * beyond 65504 it is infinite, below 6e-8 it is 0.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP. */
+int32_t mega_moe_adapter_workspace_bytes(int64_t rows, int32_t rank, uint64_t* bytes_out /* host */);
+int32_t mega_moe_adapter_forward(const void* x, const void* w, const void* a, const void* b, const float* scales,
+                                 const int32_t* offsets, const int32_t* adapter, void* y, int64_t rows, int32_t n,
+                                 int32_t k, int32_t rank, int32_t requests, int32_t adapters, int32_t dtype,
+                                 void* workspace, uint64_t workspace_bytes, uint32_t* device_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -117,3 +117,31 @@ def test_router_python_checks():
                  lambda: mm.router_backward(x[:, :2], x, x[:, :2].long()), lambda: mm.router_backward(x, x, None)):
         with pytest.raises(ValueError):
             call()
+
+
+def adapter_call(x=P, w=P, a=P, b=P, scales=P, off=P, adapter=P, y=P, rows=4, n=16, k=16, rank=8, requests=2, adapters=3,
+                 dtype=mm.BF16, ws=P, nbytes=1 << 40, status=None):
+    return mm.lib().mega_moe_adapter_forward(x, w, a, b, scales, off, adapter, y, rows, n, k, rank, requests, adapters,
+                                             dtype, ws, nbytes, status, None)
+
+
+def test_adapter_refusals():
+    for name in ("x", "w", "a", "b", "scales", "off", "adapter", "y", "ws"):
+        assert adapter_call(**{name: None}) == mm.ERR_INVALID_ARG, name
+        assert adapter_call(**{name: ctypes.c_void_p(4098)}) == mm.ERR_INVALID_ARG, name
+    for kw in (dict(rows=-1), dict(n=-8), dict(k=-8), dict(rank=-8), dict(requests=-1), dict(adapters=-1),
+               dict(status=ctypes.c_void_p(4097))):
+        assert adapter_call(**kw) == mm.ERR_INVALID_ARG, kw
+    for kw in (dict(rank=0), dict(rank=12), dict(rank=264), dict(n=12), dict(k=20), dict(n=65544), dict(adapters=0),
+               dict(adapters=65537), dict(requests=4097), dict(dtype=mm.FP32), dict(rows=(1 << 26) + 1)):
+        assert adapter_call(**kw) == mm.ERR_UNSUPPORTED, kw
+    assert adapter_call(nbytes=mm.mega_moe_adapter_workspace_bytes(4, 8) - 1) == mm.ERR_WORKSPACE_TOO_SMALL
+    assert adapter_call(rows=0, x=None, y=None) == mm.OK
+    out = ctypes.c_uint64(0)
+    lib = mm.lib()
+    assert lib.mega_moe_adapter_workspace_bytes(4, 8, None) == mm.ERR_INVALID_ARG
+    assert lib.mega_moe_adapter_workspace_bytes(-1, 8, ctypes.byref(out)) == mm.ERR_INVALID_ARG
+    assert lib.mega_moe_adapter_workspace_bytes(4, 12, ctypes.byref(out)) == mm.ERR_UNSUPPORTED
+    x = torch.zeros(4, 16)
+    with pytest.raises(ValueError):
+        mm.adapter_forward(x, x, x, x, x, x, x)
