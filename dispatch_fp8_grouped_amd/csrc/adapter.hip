@@ -43,13 +43,12 @@ __device__ __forceinline__ void store_split(const AdapterArgs& g, int64_t m, int
 }
 
 // v = scale * x a^T for one tile of a request's rows
-template <class T, int BM, int BN, int WM, int WN, int NST>
-__global__ __launch_bounds__(WM * WN * 64) void adapter_down_kernel(AdapterArgs g) {
-    using L = TileLoop<T, false, false, BM, BN, WM, WN, NST>;
+template <class L, class T, int BM, int BN>
+__global__ __launch_bounds__(L::kThreads) void adapter_down_kernel(AdapterArgs g) {
     __shared__ __align__(1024) uint8_t smem[L::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (blockIdx.x == 0 && g.status)
-        for (int r = threadIdx.x; r < g.requests; r += WM * WN * 64)
+        for (int r = threadIdx.x; r < g.requests; r += L::kThreads)
             if (g.adapter[r] < -1 || g.adapter[r] >= g.adapters) atomicOr(g.status, MEGA_MOE_STATUS_BAD_EXPERT_ID);
     const TileMap<BM> map(g.off, g.requests, g.rows, (g.rank + BN - 1) / BN, 8, lane, blockIdx.x ? nullptr : g.status);
     const int tile = xcd_tile(blockIdx.x, map.total);
@@ -59,18 +58,17 @@ __global__ __launch_bounds__(WM * WN * 64) void adapter_down_kernel(AdapterArgs 
     const int ad = __builtin_amdgcn_readfirstlane(adapter_of(g, t.g));
     if (ad < 0) return;
     const int m0 = t.mt * BM, c0 = t.nt * BN;
-    const KcTile<BM, L::kWaves> P(g.x + (size_t)(t.lo + m0) * g.k, t.cnt - m0, g.k, g.k, wave, lane);
-    const KcTile<BN, L::kWaves> Q(g.a + ((size_t)ad * g.rank + c0) * g.k, g.rank - c0, g.k, g.k, wave, lane);
+    const Operand P{g.x + (size_t)(t.lo + m0) * g.k, t.cnt - m0, g.k, g.k};
+    const Operand Q{g.a + ((size_t)ad * g.rank + c0) * g.k, g.rank - c0, g.k, g.k};
     f32x4 acc[L::QI][L::MI];
-    L::run(P, Q, (g.k + kStepK - 1) / kStepK, smem, wave, lane, acc);
-    const int wm = wave / WN, wn = wave % WN;
+    L::run(P, Q, smem, wave, lane, acc);
     const float scale = g.scales[ad];
 #pragma unroll
     for (int j = 0; j < L::MI; ++j) {
-        const int m = m0 + (wm * L::MI + j) * 16 + (lane & 15);
+        const int m = m0 + L::row(wave, j) + (lane & 15);
 #pragma unroll
         for (int i = 0; i < L::QI; ++i) {
-            const int c = c0 + (wn * L::QI + i) * 16 + (lane >> 4) * 4;
+            const int c = c0 + L::col(wave, i) + (lane >> 4) * 4;
             if (m < t.cnt && c < g.rank) store_split<T>(g, t.lo + m, c, acc[i][j], scale);
         }
     }
@@ -92,9 +90,12 @@ __device__ __forceinline__ i32x4 row_chunk(const uint16_t* row, int c, int cols)
     return c < cols ? *reinterpret_cast<const i32x4*>(row + c) : i32x4{0, 0, 0, 0};
 }
 
-// delta[i] = v b^T for the 16 rows of v from m (clamped to the last row) and 16-column blocks of b from n0
-template <class T, int QI>
-__device__ __forceinline__ void adapter_delta(const AdapterArgs& g, int ad, int m, int n0, int lane, f32x4 (&delta)[QI]) {
+// delta[i] = v b^T for the 16 rows of v from m (clamped to the last row) and this wave's column blocks of the
+// tile from column q0
+template <class T, class L>
+__device__ __forceinline__ void adapter_delta(const AdapterArgs& g, int ad, int m, int q0, int wave, int lane,
+                                              f32x4 (&delta)[L::QI]) {
+    constexpr int QI = L::QI;
     const uint16_t* vrow = g.v + (size_t)min(m + (lane & 15), g.rows - 1) * 2 * g.rank;
     const uint16_t* b = g.b + (size_t)ad * g.n * g.rank;
 #pragma unroll
@@ -104,7 +105,7 @@ __device__ __forceinline__ void adapter_delta(const AdapterArgs& g, int ad, int 
         const i32x4 hi = row_chunk(vrow, c, g.rank), lo = row_chunk(vrow + g.rank, c, g.rank);
 #pragma unroll
         for (int i = 0; i < QI; ++i) {
-            const int n = min(n0 + i * 16 + (lane & 15), g.n - 1);
+            const int n = min(q0 + L::col(wave, i) + (lane & 15), g.n - 1);
             const i32x4 q = row_chunk(b + (size_t)n * g.rank, c, g.rank);
             delta[i] = T::mfma(q, hi, delta[i]);
             delta[i] = T::mfma(q, lo, delta[i]);
@@ -113,9 +114,8 @@ __device__ __forceinline__ void adapter_delta(const AdapterArgs& g, int ad, int 
 }
 
 // y = x w^T + v b^T, one tile per work-group
-template <class T, int BM, int BN, int WM, int WN, int NST>
-__global__ __launch_bounds__(WM * WN * 64) void adapter_up_kernel(AdapterArgs g) {
-    using L = TileLoop<T, false, false, BM, BN, WM, WN, NST>;
+template <class L, class T, int BM, int BN>
+__global__ __launch_bounds__(L::kThreads) void adapter_up_kernel(AdapterArgs g) {
     __shared__ __align__(1024) uint8_t smem[L::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ntm = (g.rows + BM - 1) / BM, ntn = (g.n + BN - 1) / BN;
@@ -123,11 +123,9 @@ __global__ __launch_bounds__(WM * WN * 64) void adapter_up_kernel(AdapterArgs g)
     if (tile < 0) return;
     const int band = tile / (ntm * 8), in = tile - band * ntm * 8, width = min(8, ntn - band * 8);
     const int m0 = in / width * BM, q0 = (band * 8 + in % width) * BN;
-    const KcTile<BM, L::kWaves> P(g.x + (size_t)m0 * g.k, g.rows - m0, g.k, g.k, wave, lane);
-    const KcTile<BN, L::kWaves> Q(g.w + (size_t)q0 * g.k, g.n - q0, g.k, g.k, wave, lane);
+    const Operand P{g.x + (size_t)m0 * g.k, g.rows - m0, g.k, g.k}, Q{g.w + (size_t)q0 * g.k, g.n - q0, g.k, g.k};
     f32x4 acc[L::QI][L::MI];
-    L::run(P, Q, (g.k + kStepK - 1) / kStepK, smem, wave, lane, acc);
-    const int wm = wave / WN, wn = wave % WN, mw = m0 + wm * L::MI * 16, qw = q0 + wn * L::QI * 16;
+    L::run(P, Q, smem, wave, lane, acc);
     // the requests that own rows of this tile, in order
     for (int r = first_request(g, m0, lane); r < g.requests; ++r) {
         int lo, cnt;
@@ -140,27 +138,17 @@ __global__ __launch_bounds__(WM * WN * 64) void adapter_up_kernel(AdapterArgs g)
         if (ad < 0) continue;
 #pragma unroll
         for (int j = 0; j < L::MI; ++j) {
-            const int mj = mw + j * 16, m = mj + (lane & 15);
+            const int mj = m0 + L::row(wave, j), m = mj + (lane & 15);
             if (lo >= mj + 16 || lo + cnt <= mj) continue;
             f32x4 delta[L::QI];
-            adapter_delta<T>(g, ad, mj, qw, lane, delta);
+            adapter_delta<T, L>(g, ad, mj, q0, wave, lane, delta);
             // only this request's rows: another request's infinity must not reach a row by way of 0 * inf
             const bool mine = m >= lo && m < lo + cnt;
 #pragma unroll
             for (int i = 0; i < L::QI; ++i) acc[i][j] += mine ? delta[i] : f32x4{0.f, 0.f, 0.f, 0.f};
         }
     }
-#pragma unroll
-    for (int j = 0; j < L::MI; ++j) {
-        const int m = mw + j * 16 + (lane & 15);
-#pragma unroll
-        for (int i = 0; i < L::QI; ++i) {
-            const int c = qw + i * 16 + (lane >> 4) * 4;
-            const f32x4 s = acc[i][j];
-            if (m < g.rows && c < g.n)
-                *reinterpret_cast<u32x2*>(g.y + (size_t)m * g.n + c) = u32x2{T::pack(s[0], s[1]), T::pack(s[2], s[3])};
-        }
-    }
+    store_halves<L, T>(acc, g.y + (size_t)m0 * g.n + q0, g.rows - m0, g.n - q0, g.n, smem, wave, lane);
 }
 
 bool aligned(const void* p, uintptr_t to) { return p && ((uintptr_t)p & (to - 1)) == 0; }
@@ -170,12 +158,12 @@ hipError_t launch_adapter(const AdapterArgs& g, hipStream_t st) {
     if (g.requests > 0) {
         constexpr int BM = 64, BN = 64;
         const int64_t tiles = ((int64_t)g.rows / BM + min(g.requests, g.rows)) * ((g.rank + BN - 1) / BN);
-        hipLaunchKernelGGL((adapter_down_kernel<T, BM, BN, 2, 2, 2>), dim3((uint32_t)((tiles + 7) / 8 * 8)), dim3(256), 0,
+        hipLaunchKernelGGL((adapter_down_kernel<TileLoop<T, false, false, BM, BN, 2, 2, 2>, T, BM, BN>), dim3((uint32_t)((tiles + 7) / 8 * 8)), dim3(256), 0,
                            st, g);
     }
     constexpr int BM = 128, BN = 128;
     const int64_t tiles = (int64_t)((g.rows + BM - 1) / BM) * ((g.n + BN - 1) / BN);
-    hipLaunchKernelGGL((adapter_up_kernel<T, BM, BN, 2, 2, 2>), dim3((uint32_t)((tiles + 7) / 8 * 8)), dim3(256), 0, st, g);
+    hipLaunchKernelGGL((adapter_up_kernel<TileLoop<T, false, false, BM, BN, 2, 2, 2>, T, BM, BN>), dim3((uint32_t)((tiles + 7) / 8 * 8)), dim3(256), 0, st, g);
     return hipGetLastError();
 }
 

@@ -22,26 +22,54 @@ struct TileLoop {
     static constexpr int kPBytes = BM * 128, kStage = (BM + BN) * 128, kLds = NST * kStage;
     static constexpr int kPInstr = BM / 8 / kWaves, kQInstr = BN / 8 / kWaves, kInstr = kPInstr + kQInstr;
 
-    static __device__ __forceinline__ void frags(const uint8_t* st, int kk, int wm, int wn, int lane, i32x4 (&p)[MI],
-                                                 i32x4 (&q)[QI]) {
-#pragma unroll
-        for (int i = 0; i < QI; ++i)
-            q[i] = kQKs ? ks_frag<BN>(st + kPBytes, wn * QI + i, kk, lane) : kc_frag(st + kPBytes, wn * QI + i, kk, lane);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-            p[i] = kPKs ? ks_frag<BM>(st, wm * MI + i, kk, lane) : kc_frag(st, wm * MI + i, kk, lane);
+    // Tile row of accumulator column j, tile column of accumulator row i (first of 16)
+    static __device__ __forceinline__ int row(int wave, int j) { return (wave / WN * MI + j) * 16; }
+    static __device__ __forceinline__ int col(int wave, int i) { return (wave % WN * QI + i) * 16; }
+    using Acc = f32x4;
+    static constexpr int kRun = QI;       // accumulator rows i whose columns follow each other in the tile
+    // Fragment r of half kk of a stage: 0 .. QI-1 are Q's, then P's.
+    static __device__ __forceinline__ void read(int r, const uint8_t* st, int kk, int wm, int wn, int lane, i32x4 (&p)[MI],
+                                                i32x4 (&q)[QI]) {
+        if (r < QI)
+            q[r] = kQKs ? ks_frag<BN>(st + kPBytes, wn * QI + r, kk, lane) : kc_frag(st + kPBytes, wn * QI + r, kk, lane);
+        else
+            p[r - QI] = kPKs ? ks_frag<BM>(st, wm * MI + r - QI, kk, lane) : kc_frag(st, wm * MI + r - QI, kk, lane);
     }
-    static __device__ __forceinline__ void multiply(const i32x4 (&p)[MI], const i32x4 (&q)[QI], f32x4 (&acc)[QI][MI]) {
+    // The MFMAs of one half, with `reads` fragment reads and `loads` DMA instructions spread between them in the
+    // order they are written here (sched_barrier: left alone, the compiler gathers the reads right before
+    // their use).  The reads end three quarters of the way through, so the last ones arrive under the rest.
+    template <int reads, int loads, class R, class D>
+    static __device__ __forceinline__ void multiply(const i32x4 (&p)[MI], const i32x4 (&q)[QI], f32x4 (&acc)[QI][MI], R read_one,
+                                                    D load_one) {
+        constexpr int n = QI * MI;
 #pragma unroll
-        for (int i = 0; i < QI; ++i)
+        for (int u = 0; u < n; ++u) {
+            // walk the blocks back and forth: consecutive MFMAs share a fragment
+            const int i = u / MI, j = i & 1 ? MI - 1 - u % MI : u % MI;
+            acc[i][j] = T::mfma(q[i], p[j], acc[i][j]);
+            bool any = false;
 #pragma unroll
-            for (int j = 0; j < MI; ++j) acc[i][j] = T::mfma(q[i], p[j], acc[i][j]);
+            for (int r = 0; r < reads; ++r)
+                if (r * (n * 3 / 4) / (reads ? reads : 1) == u) {
+                    read_one(r);
+                    any = true;
+                }
+#pragma unroll
+            for (int d = 0; d < loads; ++d)
+                if (d * n / (loads ? loads : 1) == u) {
+                    load_one(d);
+                    any = true;
+                }
+            if (any) __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
-    // PT, QT: KcTile or KsTile.  All waves take part; acc is overwritten.
-    template <class PT, class QT>
-    static __device__ __forceinline__ void run(const PT& P, const QT& Q, int steps, uint8_t* smem, int wave, int lane,
+    // All waves take part; acc is overwritten.
+    static __device__ __forceinline__ void run(const Operand& po, const Operand& qo, uint8_t* smem, int wave, int lane,
                                                f32x4 (&acc)[QI][MI]) {
-        const int wm = wave / WN, wn = wave % WN;
+        const auto P = PartOf<kPKs, BM, kWaves>::make(po, 0, wave, lane);
+        const auto Q = PartOf<kQKs, BN, kWaves>::make(qo, 0, wave, lane);
+        const int steps = (po.len + kStepK - 1) / kStepK, wm = wave / WN, wn = wave % WN;
         const uint32_t lds = lds_byte(smem);
 #pragma unroll
         for (int i = 0; i < QI; ++i)
@@ -49,27 +77,246 @@ struct TileLoop {
             for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < NST; ++s) {
-            P.load(s, lds + s * kStage, wave);
-            Q.load(s, lds + s * kStage + kPBytes, wave);
+            const auto ps = P.step(s);
+            const auto qs = Q.step(s);
+#pragma unroll
+            for (int j = 0; j < kPInstr; ++j) P.load(ps, j, lds + s * kStage, wave);
+#pragma unroll
+            for (int j = 0; j < kQInstr; ++j) Q.load(qs, j, lds + s * kStage + kPBytes, wave);
         }
         i32x4 p0[MI], q0[QI], p1[MI], q1[QI];
         wait_vm_barrier<(NST - 1) * kInstr>();
-        frags(smem, 0, wm, wn, lane, p0, q0);
+#pragma unroll
+        for (int r = 0; r < QI + MI; ++r) read(r, smem, 0, wm, wn, lane, p0, q0);
         int cur = 0;
         for (int s = 0; s < steps; ++s) {
             const int nxt = cur + 1 == NST ? 0 : cur + 1;
-            frags(smem + cur * kStage, 1, wm, wn, lane, p1, q1);
-            multiply(p0, q0, acc);
+            const uint8_t *here = smem + cur * kStage, *next = smem + nxt * kStage;
+            multiply<QI + MI, 0>(p0, q0, acc, [&](int r) { read(r, here, 1, wm, wn, lane, p1, q1); }, [](int) {});
             wait_vm_barrier<(NST - 2) * kInstr>();
-            P.load(s + NST, lds + cur * kStage, wave);
-            Q.load(s + NST, lds + cur * kStage + kPBytes, wave);
-            frags(smem + nxt * kStage, 0, wm, wn, lane, p0, q0);
-            multiply(p1, q1, acc);
+            __builtin_amdgcn_sched_barrier(0);
+            const auto ps = P.step(s + NST);
+            const auto qs = Q.step(s + NST);
+            const uint32_t to = lds + cur * kStage;
+            multiply<QI + MI, kInstr>(p1, q1, acc, [&](int r) { read(r, next, 0, wm, wn, lane, p0, q0); },
+                                      [&](int d) {
+                                          if (d < kPInstr) P.load(ps, d, to, wave);
+                                          else Q.load(qs, d - kPInstr, to + kPBytes, wave);
+                                      });
             cur = nxt;
         }
         // the loads past the end still write zeros to LDS: nothing may outlive the work-group or meet a reuse
         wait_vm_barrier<0>();
     }
 };
+
+// The product loop for large tiles.  P and Q are each cut into two halves of rows (columns), four LDS regions per
+// step and two buffers of each, and a wave owns a part of both halves, so a step is four quadrants P h x Q g:
+//   A: (P0 Q0), (P0 Q1), reading Q1 and then P1 of this step from LDS
+//   B: (P1 Q0), (P1 Q1), reading P0 and then Q0 of the next step
+// A region is free as soon as its fragments are in registers: what A reads is refilled from B on with the step
+// after next, what B reads from the next A on.  Every DMA so has one and a half steps to arrive, where a loop
+// that frees whole stages gives it one with the same LDS; half of the time of that loop was this wait.
+template <class T, bool kPKs, bool kQKs, int BM, int BN, int WM, int WN>
+struct QuadLoop {
+    static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
+    static constexpr int MI = BM / 16 / WM, QI = BN / 16 / WN, MH = MI / 2, QH = QI / 2;
+    static constexpr int kPHalf = BM / 2 * 128, kQHalf = BN / 2 * 128, kLds = 4 * (kPHalf + kQHalf);
+    static constexpr int kPInstr = BM / 16 / kWaves, kQInstr = BN / 16 / kWaves, kInstr = kPInstr + kQInstr;
+    static constexpr int kQuad = MH * QH * 2;                 // MFMAs of a quadrant
+    // LDS: P half h of buffer b, then Q half g of buffer b
+    static constexpr int p_at(int b, int h) { return (b * 2 + h) * kPHalf; }
+    static constexpr int q_at(int b, int g) { return 4 * kPHalf + (b * 2 + g) * kQHalf; }
+    static __device__ __forceinline__ int row(int wave, int j) { return j / MH * (BM / 2) + (wave / WN * MH + j % MH) * 16; }
+    static __device__ __forceinline__ int col(int wave, int i) { return i / QH * (BN / 2) + (wave % WN * QH + i % QH) * 16; }
+
+    using Acc = f32x4;
+    static constexpr int kRun = QH;       // accumulator rows i whose columns follow each other in the tile
+
+    // Fragment r of a half: r / (blocks per half) is the half of the step, kk
+    static __device__ __forceinline__ void read_p(int r, const uint8_t* at, int wm, int lane, i32x4 (&p)[2][MH]) {
+        const int kk = r / MH, j = r % MH;
+        p[kk][j] = kPKs ? ks_frag<BM / 2>(at, wm * MH + j, kk, lane) : kc_frag(at, wm * MH + j, kk, lane);
+    }
+    static __device__ __forceinline__ void read_q(int r, const uint8_t* at, int wn, int lane, i32x4 (&q)[2][QH]) {
+        const int kk = r / QH, i = r % QH;
+        q[kk][i] = kQKs ? ks_frag<BN / 2>(at, wn * QH + i, kk, lane) : kc_frag(at, wn * QH + i, kk, lane);
+    }
+    // Two quadrants' MFMAs, P half h with Q halves 0 and 1; between them the reads first(r) after every second MFMA,
+    // second(r) from MFMA `from` on after every `every`, and the DMA instructions, in the order written here.
+    template <int h, int first_n, int second_n, int from, int every, class F, class S, class D>
+    static __device__ __forceinline__ void multiply(const i32x4 (&p)[2][MH], const i32x4 (&q0)[2][QH], const i32x4 (&q1)[2][QH],
+                                                    f32x4 (&acc)[QI][MI], F first, S second, D load_one) {
+#pragma unroll
+        for (int u = 0; u < 2 * kQuad; ++u) {
+            const int g = u / kQuad, v = u % kQuad, kk = v / (MH * QH), i = v / MH % QH;
+            const int j = i & 1 ? MH - 1 - v % MH : v % MH;
+            acc[g * QH + i][h * MH + j] = T::mfma(g ? q1[kk][i] : q0[kk][i], p[kk][j], acc[g * QH + i][h * MH + j]);
+            bool any = false;
+#pragma unroll
+            for (int r = 0; r < first_n; ++r)
+                if (2 * r == u) {
+                    first(r);
+                    any = true;
+                }
+#pragma unroll
+            for (int r = 0; r < second_n; ++r)
+                if (from + every * r == u) {
+                    second(r);
+                    any = true;
+                }
+#pragma unroll
+            for (int d = 0; d < kInstr; ++d)
+                if (d * kQuad / kInstr == u) {
+                    load_one(d);
+                    any = true;
+                }
+            if (any) __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // All waves take part; acc is overwritten.
+    static __device__ __forceinline__ void run(const Operand& po, const Operand& qo, uint8_t* smem, int wave, int lane,
+                                               f32x4 (&acc)[QI][MI]) {
+        const auto P0 = PartOf<kPKs, BM / 2, kWaves>::make(po, 0, wave, lane), P1 = PartOf<kPKs, BM / 2, kWaves>::make(po, BM / 2, wave, lane);
+        const auto Q0 = PartOf<kQKs, BN / 2, kWaves>::make(qo, 0, wave, lane), Q1 = PartOf<kQKs, BN / 2, kWaves>::make(qo, BN / 2, wave, lane);
+        const int steps = (po.len + kStepK - 1) / kStepK, wm = wave / WN, wn = wave % WN;
+        const uint32_t lds = lds_byte(smem);
+#pragma unroll
+        for (int i = 0; i < QI; ++i)
+#pragma unroll
+            for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto load = [&](const auto& P, const auto& Q, int s, int p_to, int q_to) {
+            const auto ps = P.step(s);
+            const auto qs = Q.step(s);
+#pragma unroll
+            for (int d = 0; d < kPInstr; ++d) P.load(ps, d, lds + p_to, wave);
+#pragma unroll
+            for (int d = 0; d < kQInstr; ++d) Q.load(qs, d, lds + q_to, wave);
+        };
+        // groups of DMA instructions in the order of their use: (P0 Q0) of step 0, (P1 Q1) of 0, (P0 Q0) of 1, ...
+        load(P0, Q0, 0, p_at(0, 0), q_at(0, 0));
+        load(P1, Q1, 0, p_at(0, 1), q_at(0, 1));
+        load(P0, Q0, 1, p_at(1, 0), q_at(1, 0));
+        load(P1, Q1, 1, p_at(1, 1), q_at(1, 1));
+        i32x4 p0[2][MH], p1[2][MH], q0[2][QH], q1[2][QH];
+        wait_vm_barrier<3 * kInstr>();
+#pragma unroll
+        for (int r = 0; r < 2 * MH; ++r) read_p(r, smem + p_at(0, 0), wm, lane, p0);
+#pragma unroll
+        for (int r = 0; r < 2 * QH; ++r) read_q(r, smem + q_at(0, 0), wn, lane, q0);
+        for (int s = 0; s < steps; ++s) {
+            const int b = s & 1;
+            const int pb = b * 2 * kPHalf, qb = b * 2 * kQHalf, pn = 2 * kPHalf - pb, qn = 2 * kQHalf - qb;
+            // A: (P1 Q1) of this step has landed; (P0 Q0) of this step is in everybody's registers: refill its buffer
+            wait_vm_barrier<2 * kInstr>();
+            __builtin_amdgcn_sched_barrier(0);
+            {
+                const auto ps = P0.step(s + 2);
+                const auto qs = Q0.step(s + 2);
+                multiply<0, 2 * QH, 2 * MH, 4 * QH, 2>(
+                    p0, q0, q1, acc, [&](int r) { read_q(r, smem + q_at(0, 1) + qb, wn, lane, q1); },
+                    [&](int r) { read_p(r, smem + p_at(0, 1) + pb, wm, lane, p1); },
+                    [&](int d) {
+                        if (d < kPInstr) P0.load(ps, d, lds + p_at(0, 0) + pb, wave);
+                        else Q0.load(qs, d - kPInstr, lds + q_at(0, 0) + qb, wave);
+                    });
+            }
+            // B: (P0 Q0) of the next step has landed; (P1 Q1) of this step is in registers
+            wait_vm_barrier<2 * kInstr>();
+            __builtin_amdgcn_sched_barrier(0);
+            {
+                const auto ps = P1.step(s + 2);
+                const auto qs = Q1.step(s + 2);
+                multiply<1, 2 * MH, 2 * QH, kQuad, 1>(
+                    p1, q0, q1, acc, [&](int r) { read_p(r, smem + p_at(0, 0) + pn, wm, lane, p0); },
+                    [&](int r) { read_q(r, smem + q_at(0, 0) + qn, wn, lane, q0); },
+                    [&](int d) {
+                        if (d < kPInstr) P1.load(ps, d, lds + p_at(0, 1) + pb, wave);
+                        else Q1.load(qs, d - kPInstr, lds + q_at(0, 1) + qb, wave);
+                    });
+            }
+        }
+        wait_vm_barrier<0>();
+    }
+};
+
+// The epilogue: the accumulators of a wave go through its share of LDS (the stages are free by now), 16 rows of one
+// run of columns at a time, so that a store instruction covers whole rows of the run, 16 bytes a lane.  Straight
+// from the accumulators it would touch 16 rows by 32 (fp32: 64) bytes; those 256 instructions of 16 partial lines
+// each took 7 us of a 256 x 256 tile.  put(place in the row, row, column, lane's 16 bytes) is called for what exists.
+// kBytes: of an output value.
+template <class L, int kBytes, class W, class P>
+__device__ __forceinline__ void store_tile(const typename L::Acc (&acc)[L::QI][L::MI], uint8_t* smem, int rows, int cols, int wave,
+                                           int lane, W write_lane, P put) {
+    constexpr int kRun = L::kRun, kRow = 16 * kRun * kBytes, kStride = kRow + 16, kBlock = 16 * kStride;
+    constexpr int kShare = L::kLds / L::kWaves / 16 * 16, kSlots = kShare / kBlock;
+    static_assert(kSlots >= 1, "a block of rows fits a wave's share of LDS");
+    constexpr int kChunks = kRow / 16, kPer = 16 / kBytes;        // 16-byte chunks of a row, values of a chunk
+    uint8_t* mine = smem + wave * kShare;
+#pragma unroll
+    for (int j = 0; j < L::MI; ++j)
+#pragma unroll
+        for (int run = 0; run < L::QI / kRun; ++run) {
+            // a wave's LDS accesses are served in order: a slot is written again only after its reads
+            uint8_t* slot = mine + (j * (L::QI / kRun) + run) % kSlots * kBlock;
+#pragma unroll
+            for (int i = 0; i < kRun; ++i)
+                write_lane(slot + (lane & 15) * kStride + (i * 16 + (lane >> 4) * 4) * kBytes, acc[run * kRun + i][j]);
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int t = 0; t < (16 * kChunks + 63) / 64; ++t) {
+                const int at = t * 64 + lane, r = at / kChunks, c = at % kChunks;
+                const int m = L::row(wave, j) + r, col = L::col(wave, run * kRun) + c * kPer;
+                if (r < 16 && m < rows && col < cols) put(m, col, *reinterpret_cast<const i32x4*>(slot + r * kStride + c * 16));
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+}
+// 16-bit rows: out points at the tile's first row and column, ld values apart.
+template <class L, class T>
+__device__ __forceinline__ void store_halves(const typename L::Acc (&acc)[L::QI][L::MI], uint16_t* out, int rows, int cols, int ld,
+                                             uint8_t* smem, int wave, int lane) {
+    store_tile<L, 2>(
+        acc, smem, rows, cols, wave, lane,
+        [](uint8_t* p, f32x4 v) { *reinterpret_cast<u32x2*>(p) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])}; },
+        [&](int m, int c, i32x4 v) { *reinterpret_cast<i32x4*>(out + (size_t)m * ld + c) = v; });
+}
+
+// Which tile shape a row product of these sizes runs with (forward and backward of the groups, the adapters'
+// shared product).  The time is estimated as `fixed` + steps * (a tile's time per step) * (rounds of tiles over the
+// CUs), with the microseconds that every shape measured: `alone` with one tile to a CU, `full` with `resident` tiles
+// on every CU (512 products of 4096 x 7168 and smaller, bf16).  The shapes, at 32768 x 4096 x 7168 over 32 groups:
+// 256 x 256 1.77 ms, 128 x 256 2.03, 64 x 128 3.14, 32 x 128 5.5, 32 x 64 5.1; at 512 x 512 x 512 over 4 groups:
+// 14.3, 9.9, 7.4, 6.2, 5.4 us; at 1024 x 7168 x 2048 over 32 groups (weights streamed) 210, 201, 183, 191, 202 us.
+struct RowShape {
+    int bm, bn, resident;
+    double fixed, alone, full;
+};
+constexpr RowShape kRowShapes[] = {{256, 256, 1, 8.5, 1.08, 1.70},
+                                   {128, 256, 1, 5.5, 0.58, 1.02},
+                                   {64, 128, 2, 4.2, 0.40, 0.84},
+                                   {32, 128, 2, 3.8, 0.29, 0.715},
+                                   {32, 64, 2, 3.6, 0.21, 0.35}};
+// choices: how many of them the product has.  Groups end inside a tile, half a tile to a group on average.
+inline int pick_row_shape(int rows, int cols, int depth, int groups, int choices) {
+    int best = 0;
+    double least = 0;
+    const int used = groups < rows ? groups : rows;
+    const double steps = (depth + kStepK - 1) / kStepK;
+    for (int i = 0; i < choices; ++i) {
+        const RowShape& s = kRowShapes[i];
+        double row_tiles = groups == 1 ? (rows + s.bm - 1) / s.bm : (double)rows / s.bm + 0.5 * used;
+        if (row_tiles < used) row_tiles = used;
+        const double tiles = row_tiles * ((cols + s.bn - 1) / s.bn), rounds = tiles / (256.0 * s.resident);
+        const double per_step = tiles <= 256 ? s.alone : s.full * (rounds > 1 ? (double)(int64_t)(rounds + 0.95) : 1.0);
+        const double t = s.fixed + steps * per_step;
+        if (i == 0 || t < least) {
+            least = t;
+            best = i;
+        }
+    }
+    return best;
+}
 
 }  // namespace mm

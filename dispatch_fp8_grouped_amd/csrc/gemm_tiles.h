@@ -81,10 +81,6 @@ __device__ __forceinline__ void dma_rows(u32x4 desc, uint32_t off, uint32_t dst)
     asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :: "v"(off), "s"(desc), "s"(dst) : "memory", "m0");
 }
-__device__ __forceinline__ void dma_rows_nt(u32x4 desc, uint32_t off, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds"
-                 :: "v"(off), "s"(desc), "s"(dst) : "memory", "m0");
-}
 // At most N of this wave's vector-memory operations still outstanding and its LDS reads returned; then barrier.
 template <int N>
 __device__ __forceinline__ void wait_vm_barrier() {
@@ -97,10 +93,12 @@ __device__ __forceinline__ void wait_vm() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-// KC: 16-byte chunk c of row r sits at position c ^ kc_swz(r), which puts the 16 rows of one fragment read into
-// 16 different 16-byte bank slots.  KS: 32-byte pair p of contraction row r sits at p ^ ks_swz(r); the eight
+// KC: 16-byte chunk c of row r sits at position c ^ kc_swz(r).  A ds_read_b128 is served in four passes of 16
+// lanes, each over all 64 banks: one pass takes eight rows of one lane group's chunk c and the other eight rows
+// of its neighbour's, c ^ 1.  With r / 2 as the swizzle those 16 lanes meet 16 different 16-byte slots, whichever eight
+// rows they are (r ^ (r / 8), which suits 16 lanes of one chunk, stalled half of the LDS-active cycles).  KS: 32-byte pair p of contraction row r sits at p ^ ks_swz(r); the eight
 // rows {0..3, 8..11} (or {4..7, 12..15}) that half a wave reads at once get eight different 32-byte slots.
-__device__ __forceinline__ int kc_swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int kc_swz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int ks_swz(int r) { return (r & 3) | ((r >> 1) & 4); }
 
 // The DMA of one KC operand tile of ROWS rows by WAVES waves; one instruction covers 8 rows.
@@ -115,8 +113,8 @@ struct KcTile {
     int len;              // contraction length
     __device__ __forceinline__ KcTile(const void* p, int rows, int ld, int length, int wave, int lane) {
         base = static_cast<const char*>(p);
-        bytes = (uint32_t)min(rows, ROWS) * (uint32_t)(ld * 2);
-        len = length;
+        bytes = (uint32_t)max(min(rows, ROWS), 0) * (uint32_t)(ld * 2);
+        len = bytes ? length : 0;
         const int r0 = wave * 8 + (lane >> 3), chunk = (lane & 7) ^ kc_swz(r0);
         col = chunk * 8;
 #pragma unroll
@@ -125,19 +123,20 @@ struct KcTile {
             off[j] = (uint32_t)(r0 + j * WAVES * 8) * (uint32_t)(ld * 2) + chunk * 16;
         }
     }
-    // step s into LDS at `lds` (the operand's tile of a stage)
-    template <bool kNt = false>
-    __device__ __forceinline__ void load(int s, uint32_t lds, int wave) const {
+    // What the DMA of step s needs: the descriptor, and whether this lane lies past the end of the rows.
+    struct Step {
+        u32x4 desc;
+        bool cut;
+    };
+    __device__ __forceinline__ Step step(int s) const {
         const int k0 = s * kStepK;
         const bool live = k0 < len;
-        const u32x4 d = buffer_of(base + (live ? (size_t)k0 * 2 : 0), live ? bytes - (uint32_t)k0 * 2u : 0u);
-        const bool cut = k0 + col >= len;       // past the end of the rows: zeros (len is a multiple of 8)
-#pragma unroll
-        for (int j = 0; j < kInstr; ++j) {
-            const uint32_t o = cut ? kPastEnd : off[j];
-            if (kNt) dma_rows_nt(d, o, lds + (wave + j * WAVES) * 1024);
-            else dma_rows(d, o, lds + (wave + j * WAVES) * 1024);
-        }
+        // len is a multiple of 8: a lane's 16 bytes are all inside or all past the end
+        return Step{buffer_of(base + (live ? (size_t)k0 * 2 : 0), live ? bytes - (uint32_t)k0 * 2u : 0u), k0 + col >= len};
+    }
+    // DMA instruction j of a step into LDS at `lds` (the operand's tile of a stage)
+    __device__ __forceinline__ void load(const Step& t, int j, uint32_t lds, int wave) const {
+        dma_rows(t.desc, t.cut ? kPastEnd : off[j], lds + (wave + j * WAVES) * 1024);
     }
 };
 
@@ -145,7 +144,8 @@ struct KcTile {
 template <int W, int WAVES>
 struct KsTile {
     static constexpr int kRowsPerInstr = 512 / W, kInstr = kStepK / kRowsPerInstr / WAVES, kBytes = W * 128;
-    static_assert(kInstr >= 1 && (kRowsPerInstr * WAVES) % 16 == 0, "the swizzle must not change with j");
+    static_assert(W >= 128, "eight 32-byte pairs to swizzle");
+    static_assert(kInstr >= 1 && (kInstr == 1 || (kRowsPerInstr * WAVES) % 16 == 0), "the swizzle must not change with j");
     const char* base;     // contraction row 0, first column of the tile
     uint32_t off[kInstr];
     uint32_t ldb, skip;   // bytes of a memory row; bytes before the tile's first column
@@ -154,21 +154,43 @@ struct KsTile {
         ldb = (uint32_t)ld * 2u;
         skip = (uint32_t)col0 * 2u;
         base = static_cast<const char*>(p) + skip;
-        len = length;
+        len = col0 < ld ? length : 0;
         const int r0 = wave * kRowsPerInstr + lane / (W / 8), pos = lane % (W / 8);
         const int chunk = (((pos >> 1) ^ ks_swz(r0)) << 1) | (pos & 1);
 #pragma unroll
         for (int j = 0; j < kInstr; ++j) off[j] = (uint32_t)(r0 + j * WAVES * kRowsPerInstr) * ldb + chunk * 16;
     }
-    template <bool kNt = false>
-    __device__ __forceinline__ void load(int s, uint32_t lds, int wave) const {
+    struct Step {
+        u32x4 desc;
+    };
+    __device__ __forceinline__ Step step(int s) const {
         const int k0 = s * kStepK, left = min(len - k0, kStepK);
-        const u32x4 d = buffer_of(base + (left > 0 ? (size_t)k0 * ldb : 0), left > 0 ? (uint32_t)left * ldb - skip : 0u);
-#pragma unroll
-        for (int j = 0; j < kInstr; ++j) {
-            if (kNt) dma_rows_nt(d, off[j], lds + (wave + j * WAVES) * 1024);
-            else dma_rows(d, off[j], lds + (wave + j * WAVES) * 1024);
-        }
+        return Step{buffer_of(base + (left > 0 ? (size_t)k0 * ldb : 0), left > 0 ? (uint32_t)left * ldb - skip : 0u)};
+    }
+    __device__ __forceinline__ void load(const Step& t, int j, uint32_t lds, int wave) const {
+        dma_rows(t.desc, off[j], lds + (wave + j * WAVES) * 1024);
+    }
+};
+
+// One operand of a product tile.  KC: `p` points at the tile's first row, `extent` rows exist from there on.  KS:
+// `p` points at contraction row 0, the tile starts at column `extent`.
+struct Operand {
+    const uint16_t* p;
+    int extent, ld, len;      // ld: values of a memory row; len: contraction length
+};
+// The part of an operand tile that starts at its row (column) `at`
+template <bool kKs, int ROWS, int WAVES>
+struct PartOf {
+    using Type = KcTile<ROWS, WAVES>;
+    static __device__ __forceinline__ Type make(const Operand& o, int at, int wave, int lane) {
+        return Type(o.p + (size_t)at * o.ld, o.extent - at, o.ld, o.len, wave, lane);
+    }
+};
+template <int ROWS, int WAVES>
+struct PartOf<true, ROWS, WAVES> {
+    using Type = KsTile<ROWS, WAVES>;
+    static __device__ __forceinline__ Type make(const Operand& o, int at, int wave, int lane) {
+        return Type(o.p, o.extent + at, o.ld, o.len, wave, lane);
     }
 };
 

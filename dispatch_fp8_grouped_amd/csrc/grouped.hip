@@ -4,6 +4,8 @@
 //   backward_weight  dw[e] = dy_e^T x_e       P = dy columns (KS), Q = x columns (KS), contraction rows
 // The row-major weights are read as they are in all three: where the contraction runs down the memory rows
 // the fragments are transposed on their way out of LDS.
+#include <type_traits>
+
 #include "gemm_kernels.h"
 
 namespace mm {
@@ -19,11 +21,22 @@ struct GroupedArgs {
     int accumulate;
 };
 
-// forward / backward_rows: one BM x BN tile of a group's rows per work-group
-template <class T, bool kBackward, int BM, int BN, int WM, int WN, int NST>
-__global__ __launch_bounds__(WM * WN * 64) void grouped_rows_kernel(GroupedArgs a) {
-    using L = TileLoop<T, false, kBackward, BM, BN, WM, WN, NST>;
-    __shared__ __align__(1024) uint8_t smem[L::kLds];
+// One tile of out = P Q^T with loop L; `out` points at the tile's first row and column, rows and cols exist there.
+template <class L, class T>
+__device__ __forceinline__ void rows_tile(const Operand& P, const Operand& Q, uint16_t* out, int rows, int cols, int ld,
+                                          uint8_t* smem, int wave, int lane) {
+    typename L::Acc acc[L::QI][L::MI];
+    L::run(P, Q, smem, wave, lane, acc);
+    store_halves<L, T>(acc, out, rows, cols, ld, smem, wave, lane);
+}
+
+// forward / backward_rows: one BM x BN tile of a group's rows per work-group.  H is a loop over half as many rows,
+// for the last tile of a group where it has no more: groups end anywhere, and a whole tile for their last rows
+// costs half a tile per group on average.
+template <class L, class H, class T, bool kBackward, int BM, int BN>
+__global__ __launch_bounds__(L::kThreads) void grouped_rows_kernel(GroupedArgs a) {
+    static_assert(H::kThreads == L::kThreads, "one launch");
+    __shared__ __align__(1024) uint8_t smem[L::kLds > H::kLds ? L::kLds : H::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cols = kBackward ? a.k : a.n, depth = kBackward ? a.n : a.k;
     const TileMap<BM> map(a.off, a.groups, a.rows, (cols + BN - 1) / BN, 8, lane, blockIdx.x ? nullptr : a.status);
@@ -31,44 +44,41 @@ __global__ __launch_bounds__(WM * WN * 64) void grouped_rows_kernel(GroupedArgs 
     if (tile < 0) return;
     const TileAt w = map.at(tile, lane);
     if (w.g < 0) return;
-    const int m0 = w.mt * BM, q0 = w.nt * BN;
-    const KcTile<BM, L::kWaves> P(a.p + (size_t)(w.lo + m0) * depth, w.cnt - m0, depth, depth, wave, lane);
+    const int m0 = w.mt * BM, q0 = w.nt * BN, rows = w.cnt - m0;
     const uint16_t* wg = a.q + (size_t)w.g * a.n * a.k;
-    f32x4 acc[L::QI][L::MI];
-    const int steps = (depth + kStepK - 1) / kStepK;
-    if constexpr (kBackward) {
-        const KsTile<BN, L::kWaves> Q(wg, q0, a.k, a.n, wave, lane);
-        L::run(P, Q, steps, smem, wave, lane, acc);
-    } else {
-        const KcTile<BN, L::kWaves> Q(wg + (size_t)q0 * a.k, a.n - q0, a.k, a.k, wave, lane);
-        L::run(P, Q, steps, smem, wave, lane, acc);
+    const Operand P{a.p + (size_t)(w.lo + m0) * depth, rows, depth, depth};
+    const Operand Q = kBackward ? Operand{wg, q0, a.k, a.n} : Operand{wg + (size_t)q0 * a.k, a.n - q0, a.k, a.k};
+    uint16_t* out = static_cast<uint16_t*>(a.out) + (size_t)(w.lo + m0) * cols + q0;
+    if (!std::is_same<L, H>::value && rows <= BM / 2)
+        rows_tile<H, T>(P, Q, out, rows, cols - q0, cols, smem, wave, lane);
+    else
+        rows_tile<L, T>(P, Q, out, rows, cols - q0, cols, smem, wave, lane);
+}
+
+// The nth longest of at most 64 groups (equal lengths: the lower one first).
+__device__ __forceinline__ int group_by_length(const int32_t* off, int groups, int rows, int nth, int lane) {
+    int lo, cnt = -1;
+    bool bad = false;
+    if (lane < groups) group_rows(off, lane, rows, lo, cnt, bad);
+    int before = 0;
+    for (int e = 0; e < groups; ++e) {
+        const int c = __builtin_amdgcn_readlane(cnt, e);
+        before += c > cnt || (c == cnt && e < lane);
     }
-    const int wm = wave / WN, wn = wave % WN;
-    uint16_t* out = static_cast<uint16_t*>(a.out);
-#pragma unroll
-    for (int j = 0; j < L::MI; ++j) {
-        const int m = m0 + (wm * L::MI + j) * 16 + (lane & 15);
-        uint16_t* row = out + (size_t)(w.lo + m) * cols;
-#pragma unroll
-        for (int i = 0; i < L::QI; ++i) {
-            const int c = q0 + (wn * L::QI + i) * 16 + (lane >> 4) * 4;
-            const f32x4 v = acc[i][j];
-            if (m < w.cnt && c < cols)
-                *reinterpret_cast<u32x2*>(row + c) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
-        }
-    }
+    return __ffsll((unsigned long long)__ballot(lane < groups && before == nth)) - 1;
 }
 
 // backward_weight: one BM x BN tile of dw[e] per work-group
-template <class T, bool kFp32, int BM, int BN, int WM, int WN, int NST>
-__global__ __launch_bounds__(WM * WN * 64) void grouped_weight_kernel(GroupedArgs a) {
-    using L = TileLoop<T, true, true, BM, BN, WM, WN, NST>;
+template <class L, class T, bool kFp32, int BM, int BN>
+__global__ __launch_bounds__(L::kThreads) void grouped_weight_kernel(GroupedArgs a) {
     __shared__ __align__(1024) uint8_t smem[L::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ntm = (a.n + BM - 1) / BM, ntq = (a.k + BN - 1) / BN;
-    const int tile = xcd_tile(blockIdx.x, a.groups * ntm * ntq);
-    if (tile < 0) return;
-    const int g = tile / (ntm * ntq), li = tile - g * ntm * ntq;
+    // work-groups b with equal b % 8 share an XCD: each XCD takes an eighth of every group's tiles, since the
+    // groups differ in length (whole groups per XCD left the XCDs of short groups idle half of the time)
+    const int per = (ntm * ntq + 7) >> 3, b = blockIdx.x >> 3, nth = b / per, li = (blockIdx.x & 7) * per + b - nth * per;
+    if (nth >= a.groups || li >= ntm * ntq) return;
+    const int g = a.groups <= 64 ? group_by_length(a.off, a.groups, a.rows, nth, lane) : nth;
     // bands of 8 row tiles, as the row products have bands of column tiles
     const int band = li / (8 * ntq), in = li - band * 8 * ntq, width = min(8, ntm - band * 8);
     const int qt = in / width, m0 = (band * 8 + in - qt * width) * BM, q0 = qt * BN;
@@ -78,30 +88,23 @@ __global__ __launch_bounds__(WM * WN * 64) void grouped_weight_kernel(GroupedArg
     lo = __builtin_amdgcn_readfirstlane(lo);
     cnt = __builtin_amdgcn_readfirstlane(cnt);
     if (bad && li == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, MEGA_MOE_STATUS_BAD_LAYOUT);
-    f32x4 acc[L::QI][L::MI];
-    const KsTile<BM, L::kWaves> P(a.p + (size_t)lo * a.n, m0, a.n, cnt, wave, lane);
-    const KsTile<BN, L::kWaves> Q(a.q + (size_t)lo * a.k, q0, a.k, cnt, wave, lane);
     if (cnt == 0 && a.accumulate) return;
-    L::run(P, Q, (cnt + kStepK - 1) / kStepK, smem, wave, lane, acc);
-    const int wm = wave / WN, wn = wave % WN;
-#pragma unroll
-    for (int j = 0; j < L::MI; ++j) {
-        const int m = m0 + (wm * L::MI + j) * 16 + (lane & 15);
-        const size_t row = ((size_t)g * a.n + m) * a.k;
-#pragma unroll
-        for (int i = 0; i < L::QI; ++i) {
-            const int c = q0 + (wn * L::QI + i) * 16 + (lane >> 4) * 4;
-            if (m >= a.n || c >= a.k) continue;
-            f32x4 v = acc[i][j];
-            if constexpr (kFp32) {
-                f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + row + c);
-                if (a.accumulate) v += *o;
-                *o = v;
-            } else {
-                *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + row + c) =
-                    u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
-            }
-        }
+    typename L::Acc acc[L::QI][L::MI];
+    const Operand P{a.p + (size_t)lo * a.n, m0, a.n, cnt}, Q{a.q + (size_t)lo * a.k, q0, a.k, cnt};
+    L::run(P, Q, smem, wave, lane, acc);
+    const size_t at = ((size_t)g * a.n + m0) * a.k + q0;
+    if constexpr (kFp32) {
+        float* out = static_cast<float*>(a.out) + at;
+        store_tile<L, 4>(
+            acc, smem, a.n - m0, a.k - q0, wave, lane, [](uint8_t* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; },
+            [&](int m, int c, i32x4 v) {
+                f32x4* o = reinterpret_cast<f32x4*>(out + (size_t)m * a.k + c);
+                f32x4 sum = __builtin_bit_cast(f32x4, v);
+                if (a.accumulate) sum += *o;
+                *o = sum;
+            });
+    } else {
+        store_halves<L, T>(acc, static_cast<uint16_t*>(a.out) + at, a.n - m0, a.k - q0, a.k, smem, wave, lane);
     }
 }
 
@@ -121,23 +124,50 @@ int32_t check_grouped(const void* p, const void* q, const int32_t* off, const vo
     return MEGA_MOE_OK;
 }
 
-template <class T, bool kBackward>
+template <class L, class H, class T, bool kBackward, int BM, int BN>
+hipError_t launch_rows_with(const GroupedArgs& a, hipStream_t st) {
+    const int64_t tiles = ((int64_t)a.rows / BM + min(a.groups, a.rows)) * (((kBackward ? a.k : a.n) + BN - 1) / BN);
+    hipLaunchKernelGGL((grouped_rows_kernel<L, H, T, kBackward, BM, BN>), dim3((uint32_t)((tiles + 7) / 8 * 8)),
+                       dim3(L::kThreads), 0, st, a);
+    return hipGetLastError();
+}
+
+template <class T, bool B>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t st) {
-    constexpr int BM = 128, BN = 128;
-    const int64_t tiles = ((int64_t)a.rows / BM + min((int64_t)a.groups, (int64_t)a.rows)) *
-                          (((kBackward ? a.k : a.n) + BN - 1) / BN);
-    hipLaunchKernelGGL((grouped_rows_kernel<T, kBackward, BM, BN, 2, 2, 2>), dim3((uint32_t)((tiles + 7) / 8 * 8)),
-                       dim3(256), 0, st, a);
+    // a KS operand needs 128 columns: the narrowest shape is the forward's only
+    using Wide = TileLoop<T, false, B, 128, 256, 2, 4, 3>;
+    using Low = TileLoop<T, false, B, 64, 256, 1, 8, 3>;
+    using Mid = TileLoop<T, false, B, 64, 128, 1, 4, 3>;
+    using Small = TileLoop<T, false, B, 32, 128, 1, 4, 4>;
+    switch (pick_row_shape(a.rows, B ? a.k : a.n, B ? a.n : a.k, a.groups, B ? 4 : 5)) {
+        case 0: return launch_rows_with<QuadLoop<T, false, B, 256, 256, 4, 2>, Wide, T, B, 256, 256>(a, st);
+        case 1: return launch_rows_with<Wide, Low, T, B, 128, 256>(a, st);
+        case 2: return launch_rows_with<Mid, Mid, T, B, 64, 128>(a, st);
+        case 3: return launch_rows_with<Small, Small, T, B, 32, 128>(a, st);
+        default:
+            if constexpr (!B) {
+                using Least = TileLoop<T, false, false, 32, 64, 1, 4, 5>;
+                return launch_rows_with<Least, Least, T, false, 32, 64>(a, st);
+            }
+            return hipErrorInvalidValue;
+    }
+}
+
+template <class L, class T, bool kFp32, int BM, int BN>
+hipError_t launch_weight_with(const GroupedArgs& a, hipStream_t st) {
+    const int64_t tiles = (int64_t)((a.n + BM - 1) / BM) * ((a.k + BN - 1) / BN);
+    hipLaunchKernelGGL((grouped_weight_kernel<L, T, kFp32, BM, BN>), dim3((uint32_t)((tiles + 7) / 8 * 8 * a.groups)),
+                       dim3(L::kThreads), 0, st, a);
     return hipGetLastError();
 }
 
 template <class T, bool kFp32>
 hipError_t launch_weight(const GroupedArgs& a, hipStream_t st) {
-    constexpr int BM = 128, BN = 128;
-    const int64_t tiles = (int64_t)a.groups * ((a.n + BM - 1) / BM) * ((a.k + BN - 1) / BN);
-    hipLaunchKernelGGL((grouped_weight_kernel<T, kFp32, BM, BN, 2, 2, 2>), dim3((uint32_t)((tiles + 7) / 8 * 8)),
-                       dim3(256), 0, st, a);
-    return hipGetLastError();
+    // 256 x 256 tiles where they fill the CUs (16384 rows, 32 x 4096 x 7168, fp32: 1.44 ms against 1.75 with
+    // 128 x 128); below that the smaller ones, four times as many
+    const int64_t large = (int64_t)a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256);
+    if (large >= 192) return launch_weight_with<QuadLoop<T, true, true, 256, 256, 2, 4>, T, kFp32, 256, 256>(a, st);
+    return launch_weight_with<TileLoop<T, true, true, 128, 128, 2, 2, 2>, T, kFp32, 128, 128>(a, st);
 }
 
 }  // namespace

@@ -18,7 +18,8 @@ compute values and gradients and record no autograd graph.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional
+
+import dispatch_fp8_grouped_amd as _mm       # the package imports this module last
 
 BF16 = 0
 FP16 = 1
@@ -63,122 +64,119 @@ def _bind(L):
         getattr(L, name).restype = i32
 
 
-def _core():
-    import dispatch_fp8_grouped_amd as mm
-    return mm
-
-
 # --------------------------------------------------------------- the C entry points, same names
 def mega_moe_grouped_forward(x, w, offsets, y, rows, n, k, groups, dtype, device_status=None, stream=None):
-    mm = _core()
-    mm._check(mm.lib().mega_moe_grouped_forward(mm._ptr(x), mm._ptr(w), mm._ptr(offsets), mm._ptr(y), rows, n, k, groups,
-                                                dtype, mm._ptr(device_status), mm._stream(stream)),
+    _mm._check(_mm.lib().mega_moe_grouped_forward(_mm._ptr(x), _mm._ptr(w), _mm._ptr(offsets), _mm._ptr(y), rows, n, k, groups,
+                                                dtype, _mm._ptr(device_status), _mm._stream(stream)),
               "mega_moe_grouped_forward")
 
 
 def mega_moe_grouped_backward_rows(dy, w, offsets, dx, rows, n, k, groups, dtype, device_status=None, stream=None):
-    mm = _core()
-    mm._check(mm.lib().mega_moe_grouped_backward_rows(mm._ptr(dy), mm._ptr(w), mm._ptr(offsets), mm._ptr(dx), rows, n, k,
-                                                      groups, dtype, mm._ptr(device_status), mm._stream(stream)),
+    _mm._check(_mm.lib().mega_moe_grouped_backward_rows(_mm._ptr(dy), _mm._ptr(w), _mm._ptr(offsets), _mm._ptr(dx), rows, n, k,
+                                                      groups, dtype, _mm._ptr(device_status), _mm._stream(stream)),
               "mega_moe_grouped_backward_rows")
 
 
 def mega_moe_grouped_backward_weight(dy, x, offsets, dw, rows, n, k, groups, dtype, out_dtype, accumulate=False,
                                      device_status=None, stream=None):
-    mm = _core()
-    mm._check(mm.lib().mega_moe_grouped_backward_weight(mm._ptr(dy), mm._ptr(x), mm._ptr(offsets), mm._ptr(dw), rows, n,
+    _mm._check(_mm.lib().mega_moe_grouped_backward_weight(_mm._ptr(dy), _mm._ptr(x), _mm._ptr(offsets), _mm._ptr(dw), rows, n,
                                                         k, groups, dtype, out_dtype, 1 if accumulate else 0,
-                                                        mm._ptr(device_status), mm._stream(stream)),
+                                                        _mm._ptr(device_status), _mm._stream(stream)),
               "mega_moe_grouped_backward_weight")
 
 
 def mega_moe_router_topk(cfg: mega_moe_router_config, logits, bias, topk_idx, topk_weights, stream=None):
-    mm = _core()
-    mm._check(mm.lib().mega_moe_router_topk(ctypes.byref(cfg), mm._ptr(logits), mm._ptr(bias), mm._ptr(topk_idx),
-                                            mm._ptr(topk_weights), mm._stream(stream)), "mega_moe_router_topk")
+    _mm._check(_mm.lib().mega_moe_router_topk(ctypes.byref(cfg), _mm._ptr(logits), _mm._ptr(bias), _mm._ptr(topk_idx),
+                                            _mm._ptr(topk_weights), _mm._stream(stream)), "mega_moe_router_topk")
 
 
 def mega_moe_router_backward(cfg: mega_moe_router_config, dweights, logits, topk_idx, dlogits, stream=None):
-    mm = _core()
-    mm._check(mm.lib().mega_moe_router_backward(ctypes.byref(cfg), mm._ptr(dweights), mm._ptr(logits), mm._ptr(topk_idx),
-                                                mm._ptr(dlogits), mm._stream(stream)), "mega_moe_router_backward")
+    _mm._check(_mm.lib().mega_moe_router_backward(ctypes.byref(cfg), _mm._ptr(dweights), _mm._ptr(logits), _mm._ptr(topk_idx),
+                                                _mm._ptr(dlogits), _mm._stream(stream)), "mega_moe_router_backward")
 
 
 def mega_moe_group_workspace_bytes(pairs: int, num_local_experts: int) -> int:
-    mm = _core()
     out = ctypes.c_uint64(0)
-    mm._check(mm.lib().mega_moe_group_workspace_bytes(pairs, num_local_experts, ctypes.byref(out)),
+    _mm._check(_mm.lib().mega_moe_group_workspace_bytes(pairs, num_local_experts, ctypes.byref(out)),
               "mega_moe_group_workspace_bytes")
     return out.value
 
 
 def mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, offsets, order, slot, workspace,
                              workspace_bytes=None, stream=None):
-    mm = _core()
     nbytes = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
-    mm._check(mm.lib().mega_moe_group_by_expert(mm._ptr(topk_idx), pairs, first_expert, num_local_experts,
-                                                mm._ptr(offsets), mm._ptr(order), mm._ptr(slot), mm._ptr(workspace),
-                                                nbytes, mm._stream(stream)), "mega_moe_group_by_expert")
+    _mm._check(_mm.lib().mega_moe_group_by_expert(_mm._ptr(topk_idx), pairs, first_expert, num_local_experts,
+                                                _mm._ptr(offsets), _mm._ptr(order), _mm._ptr(slot), _mm._ptr(workspace),
+                                                nbytes, _mm._stream(stream)), "mega_moe_group_by_expert")
 
 
 def mega_moe_adapter_workspace_bytes(rows: int, rank: int) -> int:
-    mm = _core()
     out = ctypes.c_uint64(0)
-    mm._check(mm.lib().mega_moe_adapter_workspace_bytes(rows, rank, ctypes.byref(out)), "mega_moe_adapter_workspace_bytes")
+    _mm._check(_mm.lib().mega_moe_adapter_workspace_bytes(rows, rank, ctypes.byref(out)), "mega_moe_adapter_workspace_bytes")
     return out.value
 
 
 def mega_moe_adapter_forward(x, w, a, b, scales, offsets, adapter, y, rows, n, k, rank, requests, adapters, dtype,
                              workspace, workspace_bytes=None, device_status=None, stream=None):
-    mm = _core()
     nbytes = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
-    mm._check(mm.lib().mega_moe_adapter_forward(mm._ptr(x), mm._ptr(w), mm._ptr(a), mm._ptr(b), mm._ptr(scales),
-                                                mm._ptr(offsets), mm._ptr(adapter), mm._ptr(y), rows, n, k, rank,
-                                                requests, adapters, dtype, mm._ptr(workspace), nbytes,
-                                                mm._ptr(device_status), mm._stream(stream)), "mega_moe_adapter_forward")
+    _mm._check(_mm.lib().mega_moe_adapter_forward(_mm._ptr(x), _mm._ptr(w), _mm._ptr(a), _mm._ptr(b), _mm._ptr(scales),
+                                                _mm._ptr(offsets), _mm._ptr(adapter), _mm._ptr(y), rows, n, k, rank,
+                                                requests, adapters, dtype, _mm._ptr(workspace), nbytes,
+                                                _mm._ptr(device_status), _mm._stream(stream)), "mega_moe_adapter_forward")
 
 
 # --------------------------------------------------------------- checks
 def _want(name, t, shape, dtypes, device=None):
     """t is a dense GPU tensor of this shape and one of these types (shape None: any)."""
-    ok = t is not None and t.device.type == "cuda" and t.is_contiguous() and t.dtype in dtypes
-    ok = ok and (shape is None or tuple(t.shape) == tuple(shape)) and (device is None or t.device == device)
-    if not ok:
-        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}" + (
-            "" if t.is_contiguous() else ", not contiguous")
-        types = " or ".join(str(d) for d in dtypes)
-        raise ValueError(f"{name}: want contiguous cuda {types}{'' if shape is None else ' ' + str(tuple(shape))}"
-                         f"{'' if device is None else ' on ' + str(device)}, got {got}")
+    if (t is not None and t.is_cuda and t.is_contiguous() and t.dtype in dtypes
+            and (shape is None or t.shape == shape) and (device is None or t.device == device)):
+        return
+    got = "None" if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}" + (
+        "" if t.is_contiguous() else ", not contiguous")
+    types = " or ".join(str(d) for d in dtypes)
+    raise ValueError(f"{name}: want contiguous cuda {types}{'' if shape is None else ' ' + str(tuple(shape))}"
+                     f"{'' if device is None else ' on ' + str(device)}, got {got}")
 
 
 class _Call:
-    """Makes `device` and the call's stream current, so that allocations belong to that stream."""
+    """Makes `device` and the call's stream current, so that allocations belong to that stream; `raw` is the
+    stream's handle."""
 
     def __init__(self, device, stream):
         import torch
         self.ctx = None
         if stream is None:
-            if torch.cuda.current_device() != device.index:
+            if torch._C._cuda_getDevice() != device.index:
                 self.ctx = torch.cuda.device(device)
+            # the handle of torch.cuda.current_stream(device), without making the object: a call's whole host
+            # time went from 12 to 6 us with it, and small calls are bound by that
+            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
         else:
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
             if stream.device != device:
                 raise ValueError(f"stream of {stream.device} for tensors on {device}")
             self.ctx = torch.cuda.stream(stream)
+            self.raw = stream.cuda_stream
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
+        return self.raw
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
 
+_KINDS = {}
+
+
 def _halves():
-    import torch
-    return {torch.bfloat16: BF16, torch.float16: FP16}
+    if not _KINDS:
+        import torch
+        _KINDS.update({torch.bfloat16: BF16, torch.float16: FP16})
+    return _KINDS
 
 
 def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream, call):
@@ -194,12 +192,12 @@ def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream, call):
     _want("offsets", offsets, (groups + 1,), (torch.int32,), w.device)
     if status is not None:
         _want("status", status, (1,), (torch.int32,), w.device)
-    with _Call(w.device, stream):
+    with _Call(w.device, stream) as raw:
         if out is None:
             out = torch.empty((rows, outer), dtype=w.dtype, device=w.device)
         else:
             _want("out", out, (rows, outer), (w.dtype,), w.device)
-        call(rows_in, w, offsets, out, rows, n, k, groups, kinds[w.dtype], status)
+        call(rows_in, w, offsets, out, rows, n, k, groups, kinds[w.dtype], status, raw)
     return out
 
 
@@ -237,13 +235,13 @@ def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=Fal
         raise ValueError("accumulate needs a float32 `out`")
     if status is not None:
         _want("status", status, (1,), (torch.int32,), x.device)
-    with _Call(x.device, stream):
+    with _Call(x.device, stream) as raw:
         if out is None:
             out = torch.empty((groups, n, k), dtype=dtype, device=x.device)
         else:
             _want("out", out, (groups, n, k), (dtype,), x.device)
         mega_moe_grouped_backward_weight(dy, x, offsets, out, rows, n, k, groups, kinds[x.dtype],
-                                         FP32 if dtype == torch.float32 else kinds[dtype], accumulate, status)
+                                         FP32 if dtype == torch.float32 else kinds[dtype], accumulate, status, raw)
     return out
 
 
@@ -273,10 +271,10 @@ def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_gro
     if bias is not None:
         _want("bias", bias, (cfg.num_experts,), (torch.float32,), logits.device)
     shape = (*logits.shape[:-1], max(topk, 0))
-    with _Call(logits.device, stream):
+    with _Call(logits.device, stream) as raw:
         idx = torch.empty(shape, dtype=torch.int64, device=logits.device)
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
-        mega_moe_router_topk(cfg, logits, bias, idx, weights)
+        mega_moe_router_topk(cfg, logits, bias, idx, weights, raw)
     return idx, weights
 
 
@@ -289,9 +287,9 @@ def router_backward(dweights, logits, topk_idx, score="softmax", renormalize=Tru
     cfg = _router_config(logits, topk, score, 1, 1, 1, renormalize, scale)
     _want("topk_idx", topk_idx, (*logits.shape[:-1], topk), (torch.int64,), logits.device)
     _want("dweights", dweights, (*logits.shape[:-1], topk), (torch.float32,), logits.device)
-    with _Call(logits.device, stream):
+    with _Call(logits.device, stream) as raw:
         dlogits = torch.empty_like(logits)
-        mega_moe_router_backward(cfg, dweights, logits, topk_idx, dlogits)
+        mega_moe_router_backward(cfg, dweights, logits, topk_idx, dlogits, raw)
     return dlogits
 
 
@@ -303,12 +301,13 @@ def group_by_expert(topk_idx, num_local_experts, first_expert=0, stream=None):
     _want("topk_idx", topk_idx, None, (torch.int64,))
     pairs, device = topk_idx.numel(), topk_idx.device
     nbytes = mega_moe_group_workspace_bytes(pairs, num_local_experts)
-    with _Call(device, stream):
+    with _Call(device, stream) as raw:
         offsets = torch.empty(num_local_experts + 1, dtype=torch.int32, device=device)
         order = torch.empty(pairs, dtype=torch.int32, device=device)
         slot = torch.empty(topk_idx.shape, dtype=torch.int32, device=device)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, offsets, order, slot, workspace)
+        mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, offsets, order, slot, workspace,
+                                 nbytes, raw)
     return offsets, order, slot
 
 
@@ -334,7 +333,7 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
     if status is not None:
         _want("status", status, (1,), (torch.int32,), w.device)
     nbytes = mega_moe_adapter_workspace_bytes(rows, rank)
-    with _Call(w.device, stream):
+    with _Call(w.device, stream) as raw:
         if out is None:
             out = torch.empty((rows, n), dtype=w.dtype, device=w.device)
         else:
@@ -344,5 +343,5 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
         else:
             _want("workspace", workspace, None, (torch.uint8,), w.device)
         mega_moe_adapter_forward(x, w, a, b, scales, offsets, adapter, out, rows, n, k, rank, requests, adapters,
-                                 kinds[w.dtype], workspace, None, status)
+                                 kinds[w.dtype], workspace, None, status, raw)
     return out

@@ -79,6 +79,12 @@ SHAPES = [
     ([2048], 512, 64),
     ([1] * 100 + [0] * 50 + [7] * 50, 72, 128),
     ([40] * 8, 2056, 2048),
+    # long enough for the large tiles, with groups that end just behind one, in its first and in its second half
+    ([3000, 0, 2500, 1300, 257], 4104, 200),
+    ([6000, 129, 128, 127, 1], 2056, 328),
+    ([1, 300, 8000], 520, 3080),
+    ([9000], 264, 4104),
+    ([3000, 17, 0, 900], 4104, 2056),
 ]
 
 
