@@ -1,21 +1,28 @@
 // The router around the fused layer (include/mega_moe_ops.h): the choice and weights of each token's experts,
 // the gradient of the weights, and the ordering of the chosen pairs by expert.
 //
-// Choice: one wave per token; lane l holds experts l*EPL .. l*EPL + EPL-1 (so the lowest lane of a tie holds
-// the lowest expert).  An expert's rank becomes an unsigned key whose order is the rank's order, 0 for an
-// expert that may not be chosen: 32 bits from the logit alone, 64 bits from the fp64 score + bias.  Each of the
-// K rounds takes the wave's largest high word; only where several lanes share it do the low words decide.
+// Choice: LANES lanes per token (a wave, or a quarter of one); lane l of them holds experts l*EPL .. l*EPL + EPL-1
+// (so the lowest lane of a tie holds the lowest expert).  Without a bias the logit and the expert's number make one
+// fp64 number, all different: each lane sorts its own once, and a round is a maximum over the lanes' first ones.  With
+// a bias the fp64 score + bias is the rank, as two unsigned words: a round takes the largest high word, and only
+// where several lanes share it do the low words decide.  What bounds it is instruction issue (about
+// 1000 a wave), and the rounds cost the same whether a wave serves one token or four, so many tokens take a quarter
+// wave each: 32768 tokens x 256 experts, top 8, bf16, 38 us with a wave each and 16 with a quarter (the bytes: 5).
+// Few tokens take a whole wave, whose lanes have fewer experts to walk (1024 x 256, fp32, sigmoid with bias and
+// groups: 8 us).
 //
 // Scores are computed in fp64 (exp of the C library's device functions): two scores that differ in fp32
 // logits then differ in rank, and the choice does not hang on a rounding of exp.
+#include <type_traits>
+
 #include "gemm_tiles.h"
 
 namespace mm {
 namespace {
 
-constexpr uint32_t kPairsPerWave = 256;      // pairs that one wave of the ordering ranks, 64 at a time
+constexpr int kPairsPerWave = 256;           // least pairs that one wave of the ordering places, 64 at a time
 constexpr int kOneGroupPairs = 8192;         // up to here one work-group orders everything in one launch
-constexpr int kOneGroupExperts = 512;       // 32 KB of counters
+constexpr int kOneGroupExperts = 256;       // 16 KB of counters beside 32 KB of places
 
 struct RouterArgs {
     const void* logits;
@@ -36,10 +43,36 @@ __device__ __forceinline__ float read_value(const void* p, int type, size_t i) {
     if (type == MEGA_MOE_BF16) return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
     return (float)static_cast<const _Float16*>(p)[i];
 }
-__device__ __forceinline__ void write_value(void* p, int type, size_t i, double v) {
-    if (type == MEGA_MOE_FP32) static_cast<float*>(p)[i] = (float)v;
-    else if (type == MEGA_MOE_BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16((float)v);
-    else static_cast<_Float16*>(p)[i] = (_Float16)(float)v;
+// This lane's EPL values v(j) of a row of E, wide where read_lane reads wide.
+template <int EPL, class V, class F>
+__device__ __forceinline__ void write_lane(V* row, int E, int lane, F value) {
+    constexpr int kWide = EPL * (int)sizeof(V) < 16 ? EPL : 16 / (int)sizeof(V);
+    struct __align__(kWide * sizeof(V)) Wide { V v[kWide]; };
+    const int e0 = lane * EPL;
+    if (E % EPL == 0) {
+        if (e0 >= E) return;
+#pragma unroll
+        for (int j = 0; j < EPL; j += kWide) {
+            Wide w;
+#pragma unroll
+            for (int i = 0; i < kWide; ++i) w.v[i] = value(j + i);
+            *reinterpret_cast<Wide*>(row + e0 + j) = w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (e0 + j < E) row[e0 + j] = value(j);
+    }
+}
+template <int EPL, class F>
+__device__ __forceinline__ void write_row(void* p, int type, int64_t t, int E, int lane, F v) {
+    const size_t at = (size_t)t * E;
+    if (type == MEGA_MOE_FP32)
+        write_lane<EPL>(static_cast<float*>(p) + at, E, lane, [&](int j) { return (float)v(j); });
+    else if (type == MEGA_MOE_BF16)
+        write_lane<EPL>(static_cast<uint16_t*>(p) + at, E, lane, [&](int j) { return (uint16_t)Bf16::pack((float)v(j), 0.f); });
+    else
+        write_lane<EPL>(static_cast<_Float16*>(p) + at, E, lane, [&](int j) { return (_Float16)(float)v(j); });
 }
 
 // This lane's EPL logits of a row of E; -inf past the row.  Where E is a multiple of EPL, every lane's
@@ -77,30 +110,125 @@ __device__ __forceinline__ void read_row(const void* p, int type, int64_t t, int
 __device__ __forceinline__ bool is_masked(float x) { return !(x > -__builtin_inff()); }
 __device__ __forceinline__ float clip_inf(float x) { return fminf(x, 3.402823466e38f); }
 
-// Unsigned integers in the order of the numbers (no NaN); no number maps to 0.
-__device__ __forceinline__ uint32_t order32(float x) {
-    const uint32_t u = __float_as_uint(x + 0.0f);        // -0 ranks with +0
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+// A logit and its expert as one fp64 number: the logit takes 24 of the 53 bits, the expert's number goes into the
+// low 12, so that of equal logits the lower expert's number is larger.  All are different and above -inf.
+__device__ __forceinline__ double with_expert(float x, int e) {
+    const uint64_t u = (uint64_t)__double_as_longlong((double)(x + 0.0f));        // -0 ranks with +0
+    return __longlong_as_double((long long)(u | (uint64_t)(u >> 63 ? e : MEGA_MOE_MAX_EXPERTS - 1 - e)));
 }
+__device__ __forceinline__ int expert_of(double key) {
+    const uint64_t u = (uint64_t)__double_as_longlong(key);
+    const int low = (int)(u & (MEGA_MOE_MAX_EXPERTS - 1));
+    return u >> 63 ? low : MEGA_MOE_MAX_EXPERTS - 1 - low;
+}
+static_assert(MEGA_MOE_MAX_EXPERTS == 1 << 12, "12 bits");
+
+// Sort n numbers, the largest first (Batcher's odd-even merge network; n a power of two)
+template <int n>
+__device__ __forceinline__ void sort_down(double (&v)[n]) {
+#pragma unroll
+    for (int p = 1; p < n; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < n; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < n && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const double a = v[i + j], b = v[i + j + k];
+                        v[i + j] = fmax(a, b);
+                        v[i + j + k] = fmin(a, b);
+                    }
+}
+
+// Unsigned integers in the order of the numbers (no NaN); no number maps to 0.
 __device__ __forceinline__ uint64_t order64(double x) {
     const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+// v of a lane in the other half of 2 d lanes, for a v that is the same in every run of d lanes (DPP quad
+// permutations and mirrors; the row and half-wave swaps return both halves)
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
+}
+template <int d>
+__device__ __forceinline__ uint32_t mirror(uint32_t v) {
+    static_assert(d == 1 || d == 2 || d == 4 || d == 8, "within a row of 16 lanes");
+    return d == 1 ? dpp<0xB1>(v) : d == 2 ? dpp<0x4E>(v) : d == 4 ? dpp<0x141>(v) : dpp<0x140>(v);
+}
+__device__ __forceinline__ uint32_t low_word(double v) { return (uint32_t)__double_as_longlong(v); }
+__device__ __forceinline__ uint32_t high_word(double v) { return (uint32_t)((uint64_t)__double_as_longlong(v) >> 32); }
+__device__ __forceinline__ double from_words(uint32_t lo, uint32_t hi) {
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+template <int d>
+__device__ __forceinline__ double mirror(double v) { return from_words(mirror<d>(low_word(v)), mirror<d>(high_word(v))); }
+
+// op over LANES neighbouring lanes (16 or 64), the result in all of them; op's order is fixed by the lane numbers
+template <int LANES, class F>
+__device__ __forceinline__ uint32_t all_of(uint32_t v, F op) {
+    v = op(v, mirror<1>(v));
+    v = op(v, mirror<2>(v));
+    v = op(v, mirror<4>(v));
+    v = op(v, mirror<8>(v));
+    if constexpr (LANES == 64) {
+        const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = op(a[0], a[1]);
+        const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = op(b[0], b[1]);
+    }
     return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+template <int LANES>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+    return all_of<LANES>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int LANES>
+__device__ __forceinline__ float max_of(float v) {
+    return __uint_as_float(all_of<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
+template <int LANES>
+__device__ __forceinline__ double max_of(double v) {
+    v = fmax(v, mirror<1>(v));
+    v = fmax(v, mirror<2>(v));
+    v = fmax(v, mirror<4>(v));
+    v = fmax(v, mirror<8>(v));
+    if constexpr (LANES == 64) {
+        auto l = __builtin_amdgcn_permlane16_swap(low_word(v), low_word(v), false, false);
+        auto h = __builtin_amdgcn_permlane16_swap(high_word(v), high_word(v), false, false);
+        v = fmax(from_words(l[0], h[0]), from_words(l[1], h[1]));
+        l = __builtin_amdgcn_permlane32_swap(low_word(v), low_word(v), false, false);
+        h = __builtin_amdgcn_permlane32_swap(high_word(v), high_word(v), false, false);
+        v = fmax(from_words(l[0], h[0]), from_words(l[1], h[1]));
+    }
     return v;
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+// Sums of fp64 (the two operands of an addition swap between lanes, which changes nothing)
+template <int LANES>
+__device__ __forceinline__ double sum_of(double v) {
+    v += mirror<1>(v);
+    v += mirror<2>(v);
+    v += mirror<4>(v);
+    v += mirror<8>(v);
+    if constexpr (LANES == 64) {
+        auto l = __builtin_amdgcn_permlane16_swap(low_word(v), low_word(v), false, false);
+        auto h = __builtin_amdgcn_permlane16_swap(high_word(v), high_word(v), false, false);
+        v = from_words(l[0], h[0]) + from_words(l[1], h[1]);
+        l = __builtin_amdgcn_permlane32_swap(low_word(v), low_word(v), false, false);
+        h = __builtin_amdgcn_permlane32_swap(high_word(v), high_word(v), false, false);
+        v = from_words(l[0], h[0]) + from_words(l[1], h[1]);
+    }
     return v;
+}
+// Lanes of this token for which `p` holds, as bits from 0
+template <int LANES>
+__device__ __forceinline__ uint64_t lanes_with(bool p) {
+    const uint64_t all = __ballot(p);
+    return LANES == 64 ? all : (all >> (__lane_id() & ~(LANES - 1))) & ((1ull << (LANES & 63)) - 1);
 }
 
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
@@ -112,13 +240,17 @@ __device__ __forceinline__ void merge_top2(double& a, double& b, double c, doubl
     a = hi;
 }
 
-// kWide: 64-bit ranks (a bias is given); waves of a work-group take consecutive tokens.
-template <int EPL, bool kSigmoid, bool kWide, bool kGroups, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void router_kernel(RouterArgs a) {
-    __shared__ double values[kGroups ? WAVES : 1][kGroups ? EPL * 64 : 1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// kWide: 64-bit ranks (a bias is given).  A work-group's tokens follow each other.
+template <int EPL, int LANES, bool kSigmoid, bool kWide, bool kGroups, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1) void router_kernel(RouterArgs a) {
+    constexpr int kTokens = WAVES * 64 / LANES;
+    __shared__ double values[kGroups ? kTokens : 1][kGroups ? EPL * LANES : 1];
+    const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES, wave = threadIdx.x >> 6;
     const double none = -__builtin_inf();
-    for (int64_t t = (int64_t)blockIdx.x * WAVES + wave; t < a.tokens; t += (int64_t)gridDim.x * WAVES) {
+    // a wave whose last tokens do not exist repeats the last one for them, and does not store
+    for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 + wave * (64 / LANES) < a.tokens; t0 += (int64_t)gridDim.x * kTokens) {
+        const bool real = t0 + mine < a.tokens;
+        const int64_t t = real ? t0 + mine : a.tokens - 1;
         float x[EPL];
         bool live[EPL];
         float top = -__builtin_inff();
@@ -129,24 +261,25 @@ __global__ __launch_bounds__(WAVES * 64) void router_kernel(RouterArgs a) {
             x[j] = clip_inf(x[j]);
             if (live[j]) top = fmaxf(top, x[j]);
         }
-        top = wave_max(top);                       // -inf where everything is masked
-        // softmax needs its sum where the scores themselves enter the result; where they are divided by
-        // the chosen ones' sum it cancels
+        // softmax needs its largest logit and its sum where the scores themselves enter the result; where they
+        // are divided by the chosen ones' sum both cancel
         const bool by_score = kWide || (kGroups && a.gtop == 2);
         double total = 1.0;
         if (!kSigmoid && (by_score || !a.renorm)) {
+            top = max_of<LANES>(top);              // -inf where everything is masked
             total = 0.0;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
                 if (live[j]) total += exp((double)x[j] - (double)top);
-            total = wave_sum(total);
+            total = sum_of<LANES>(total);
         }
-        uint32_t hi[EPL], lo[kWide ? EPL : 1];
+        uint32_t hi[kWide ? EPL : 1], lo[kWide ? EPL : 1];
+        double key[kWide ? 1 : EPL];
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = lane * EPL + j;
             double rank = x[j], worth = x[j];
-            if ((kWide || (kGroups && a.gtop == 2)) && live[j]) {
+            if (by_score && live[j]) {
                 const double s = kSigmoid ? sigmoid64(x[j]) : exp((double)x[j] - (double)top) / total;
                 worth = s;
                 if constexpr (kWide) {
@@ -155,107 +288,130 @@ __global__ __launch_bounds__(WAVES * 64) void router_kernel(RouterArgs a) {
                 }
             }
             if constexpr (kWide) {
-                const uint64_t key = live[j] ? order64(rank) : 0;
-                hi[j] = (uint32_t)(key >> 32);
-                lo[j] = (uint32_t)key;
+                const uint64_t word = live[j] ? order64(rank) : 0;
+                hi[j] = (uint32_t)(word >> 32);
+                lo[j] = (uint32_t)word;
             } else {
-                hi[j] = live[j] ? order32(x[j]) : 0;
+                key[j] = live[j] ? with_expert(x[j], e) : none;
             }
-            if constexpr (kGroups) values[wave][e] = live[j] ? worth : none;
+            if constexpr (kGroups) values[mine][e] = live[j] ? worth : none;
         }
         if constexpr (kGroups) {
             // L lanes per group (a power of two); group g's lanes are g*L .. g*L + L-1
             int L = 1;
-            while (L * 2 * a.G <= 64) L *= 2;
+            while (L * 2 * a.G <= LANES) L *= 2;
             const int size = a.E / a.G, g = lane / L;
             double first = none, second = none;
             __builtin_amdgcn_wave_barrier();
             if (g < a.G)
-                for (int i = lane % L; i < size; i += L) merge_top2(first, second, values[wave][g * size + i], none);
-            for (int d = 1; d < L; d <<= 1) {
-                const double c = __shfl_xor(first, d), e2 = __shfl_xor(second, d);
-                merge_top2(first, second, c, e2);
-            }
+                for (int i = lane % L; i < size; i += L) merge_top2(first, second, values[mine][g * size + i], none);
+            auto meet = [&](auto other) {
+                const double c = other(first), d = other(second);
+                merge_top2(first, second, c, d);
+            };
+            if (L > 1) meet([](double v) { return mirror<1>(v); });
+            if (L > 2) meet([](double v) { return mirror<2>(v); });
+            if (L > 4) meet([](double v) { return mirror<4>(v); });
+            if (L > 8) meet([](double v) { return mirror<8>(v); });
+            if (L > 16) meet([](double v) { return __shfl_xor(v, 16); });
             // a group's worth: its best, or the sum of its two best where it has two
             double worth = first;
             if (a.gtop == 2 && second > none) worth += second;
             bool open = (lane % L) == 0 && g < a.G && first > none;
             uint64_t kept = 0;                     // bit of every kept group's first lane
             for (int r = 0; r < a.kept; ++r) {
-                const uint64_t key = open ? order64(worth) : 0;
-                const uint32_t h = wave_max((uint32_t)(key >> 32));
-                const bool in = (uint32_t)(key >> 32) == h;
-                const uint32_t l = wave_max(in ? (uint32_t)key : 0u);
-                if (!(h | l)) break;
-                const uint64_t who = __ballot(in && (uint32_t)key == l);
-                const int winner = __ffsll((unsigned long long)who) - 1;
-                kept |= 1ull << winner;
-                open = open && lane != winner;
+                const double best = max_of<LANES>(open ? worth : none);
+                const uint64_t who = lanes_with<LANES>(open && worth == best);
+                if (who) {
+                    const int winner = __ffsll((unsigned long long)who) - 1;
+                    kept |= 1ull << winner;
+                    open = open && lane != winner;
+                }
             }
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
                 const int e = lane * EPL + j, at = e < a.E ? e / size * L : 0;
                 if (!((kept >> at) & 1)) {
-                    hi[j] = 0;
-                    if constexpr (kWide) lo[j] = 0;
+                    if constexpr (kWide) hi[j] = lo[j] = 0;
+                    else key[j] = none;
                 }
             }
             __builtin_amdgcn_wave_barrier();
         }
         // K rounds; lane k keeps choice k
         int chosen = -1;
-        float chosen_x = 0.f;
-        for (int k = 0; k < a.K; ++k) {
-            uint32_t bh = 0, bl = 0;
-            int bj = 0;
-            float bx = 0.f;
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                const bool better = kWide ? (hi[j] > bh || (hi[j] == bh && lo[kWide ? j : 0] > bl)) : hi[j] > bh;
-                if (better) {
-                    bh = hi[j];
-                    if constexpr (kWide) bl = lo[j];
-                    bj = j;
-                    bx = x[j];
-                }
-            }
-            const uint32_t h = wave_max(bh);
-            uint64_t who = __ballot(bh == h);
-            if (h == 0) break;                     // nothing left (a live rank's high word is never 0)
-            if (kWide && __popcll(who) > 1) {
-                const uint32_t l = wave_max(bh == h ? bl : 0u);
-                who &= __ballot(bl == l);
-            }
-            const int winner = __ffsll((unsigned long long)who) - 1;
-            const int e = __shfl(lane * EPL + bj, winner);
-            const float ex = __shfl(bx, winner);
-            if (lane == k) {
-                chosen = e;
-                chosen_x = ex;
-            }
-            if (lane == winner) {
+        if constexpr (kWide) {
+            // a live rank's high word is never 0
+            for (int k = 0; k < a.K; ++k) {
+                uint32_t bh = 0, bl = 0;
+                int bj = 0;
 #pragma unroll
                 for (int j = 0; j < EPL; ++j)
-                    if (j == bj) {
-                        hi[j] = 0;
-                        if constexpr (kWide) lo[j] = 0;
+                    if (hi[j] > bh || (hi[j] == bh && lo[j] > bl)) {
+                        bh = hi[j];
+                        bl = lo[j];
+                        bj = j;
                     }
+                const uint32_t h = max_of<LANES>(bh);
+                uint64_t who = lanes_with<LANES>(bh == h);
+                if (__any(__popcll(who) > 1)) {
+                    const uint32_t l = max_of<LANES>(bh == h ? bl : 0u);
+                    who = lanes_with<LANES>(bh == h && bl == l);
+                }
+                const int winner = h ? __ffsll((unsigned long long)who) - 1 : -1;
+                const int e = __shfl(lane * EPL + bj, (threadIdx.x & 63 & ~(LANES - 1)) + max(winner, 0));
+                if (lane == k && winner >= 0) chosen = e;
+                const int gone = lane == winner ? bj : -1;
+#pragma unroll
+                for (int j = 0; j < EPL; ++j)
+                    if (j == gone) hi[j] = lo[j] = 0;
+            }
+        } else {
+            // every lane's experts sorted once: a round looks at the lanes' first ones, and the lane that had the
+            // largest moves up.  Only the first K of a lane can be reached.
+            if constexpr (EPL > 16) {
+                // too many to sort in registers: every round walks them
+                for (int k = 0; k < a.K; ++k) {
+                    double first = none;
+#pragma unroll
+                    for (int j = 0; j < EPL; ++j) first = fmax(first, key[j]);
+                    const double best = max_of<LANES>(first);
+                    if (lane == k && best > none) chosen = expert_of(best);
+#pragma unroll
+                    for (int j = 0; j < EPL; ++j) key[j] = key[j] == best ? none : key[j];
+                }
+            } else {
+            sort_down(key);
+            auto rounds = [&](auto depth) {
+                constexpr int kDepth = decltype(depth)::value;
+                for (int k = 0; k < a.K; ++k) {
+                    const double best = max_of<LANES>(key[0]);
+                    if (lane == k && best > none) chosen = expert_of(best);
+                    const bool mine_won = key[0] == best;
+#pragma unroll
+                    for (int j = 0; j < kDepth; ++j) key[j] = mine_won ? (j + 1 < EPL ? key[j + 1 < EPL ? j + 1 : 0] : none) : key[j];
+                }
+            };
+            if (EPL > 8 && a.K <= 8) rounds(std::integral_constant<int, EPL < 8 ? EPL : 8>{});
+            else rounds(std::integral_constant<int, EPL>{});
             }
         }
+        // the chosen logit once more, from the cache
+        float chosen_x = chosen >= 0 ? clip_inf(read_value(a.logits, a.type, (size_t)t * a.E + chosen)) : -__builtin_inff();
         // renormalized, softmax's common factor cancels: taken relative to the largest chosen logit, the sum
         // cannot underflow where a bias or the groups left the largest logits out
         if (!kSigmoid && a.renorm) {
-            top = wave_max(chosen >= 0 ? chosen_x : -__builtin_inff());
+            top = max_of<LANES>(chosen_x);
             total = 1.0;
         }
         double s = 0.0;
         if (chosen >= 0)
             s = kSigmoid ? sigmoid64(chosen_x) : exp((double)chosen_x - (double)top) / total;
         if (a.renorm) {
-            const double sum = wave_sum(s);
+            const double sum = sum_of<LANES>(s);
             s = sum > 0.0 ? s / sum : 0.0;
         }
-        if (lane < a.K) {
+        if (real && lane < a.K) {
             a.idx[t * a.K + lane] = chosen;
             a.weights[t * a.K + lane] = (float)(s * (double)a.scale);
         }
@@ -268,14 +424,18 @@ __global__ __launch_bounds__(WAVES * 64) void router_kernel(RouterArgs a) {
 //   sigmoid        dlogit_i = ds_i s_i (1 - s_i)
 //   softmax        dlogit_i = s_i (ds_i - sum_j ds_j s_j); renormalized, that sum is 0
 // Only softmax without renormalizing reaches experts that were not named, and only it reads all logits
-// (kAll); in the other forms the scores' common factor cancels or does not exist.  One wave per token: lane k
-// computes the gradient of the expert that place k names, the row is put together in LDS.
-template <int EPL, bool kSigmoid, bool kAll, int WAVES>
+// (kAll); in the other forms the scores' common factor cancels or does not exist.  LANES lanes per token as in the
+// choice: lane k computes the gradient of the expert that place k names, the row is put together in LDS.
+template <int EPL, int LANES, bool kSigmoid, bool kAll, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void router_backward_kernel(RouterArgs a) {
-    __shared__ double rows[WAVES][EPL * 64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double* row = rows[wave];
-    for (int64_t t = (int64_t)blockIdx.x * WAVES + wave; t < a.tokens; t += (int64_t)gridDim.x * WAVES) {
+    constexpr int kTokens = WAVES * 64 / LANES;
+    __shared__ double rows[kTokens][EPL * LANES];
+    const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES, wave = threadIdx.x >> 6;
+    const int lane0 = threadIdx.x & 63 & ~(LANES - 1);
+    double* row = rows[mine];
+    for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 + wave * (64 / LANES) < a.tokens; t0 += (int64_t)gridDim.x * kTokens) {
+        const bool real = t0 + mine < a.tokens;
+        const int64_t t = real ? t0 + mine : a.tokens - 1;
         int64_t id = -1;
         float g = 0.f, xk = -__builtin_inff();
         if (lane < a.K) {
@@ -287,10 +447,11 @@ __global__ __launch_bounds__(WAVES * 64) void router_backward_kernel(RouterArgs 
         const int named = (int)id;
         const bool live = named >= 0 && !is_masked(xk);
         xk = clip_inf(xk);
-        float x[kAll ? EPL : 1];
+        double base[kAll ? EPL : 1];               // scores of this lane's experts
         float top;
         double total = 1.0;
         if constexpr (kAll) {
+            float x[EPL];
             read_row<EPL>(a.logits, a.type, t, a.E, lane, x);
             top = -__builtin_inff();
 #pragma unroll
@@ -298,14 +459,16 @@ __global__ __launch_bounds__(WAVES * 64) void router_backward_kernel(RouterArgs 
                 x[j] = is_masked(x[j]) ? -__builtin_inff() : clip_inf(x[j]);
                 top = fmaxf(top, x[j]);
             }
-            top = wave_max(top);
+            top = max_of<LANES>(top);
             total = 0.0;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                if (x[j] > -__builtin_inff()) total += exp((double)x[j] - (double)top);
-            total = wave_sum(total);
+            for (int j = 0; j < EPL; ++j) {
+                base[j] = x[j] > -__builtin_inff() ? exp((double)x[j] - (double)top) : 0.0;
+                total += base[j];
+            }
+            total = sum_of<LANES>(total);
         } else {
-            top = wave_max(live ? xk : -__builtin_inff());
+            top = max_of<LANES>(live ? xk : -__builtin_inff());
         }
         double s = 0.0, rest = 0.0;
         if (live) {
@@ -315,16 +478,16 @@ __global__ __launch_bounds__(WAVES * 64) void router_backward_kernel(RouterArgs 
         double G = 0.0;
         int n = 0, before = 0;
         for (int k = 0; k < a.K; ++k) {
-            const int e = __shfl(named, k);
-            const float gk = __shfl(g, k);
+            const int e = __shfl(named, lane0 + k);
+            const float gk = __shfl(g, lane0 + k);
             if (e == named) {
                 G += (double)gk;
                 ++n;
                 before += k < lane;
             }
         }
-        const double gs = wave_sum(live ? (double)g * s : 0.0);
-        const double S = a.renorm ? wave_sum(s) : 1.0;
+        const double gs = sum_of<LANES>(live ? (double)g * s : 0.0);
+        const double S = a.renorm ? sum_of<LANES>(s) : 1.0;
         double d = 0.0;
         if (live) {
             if (a.renorm) {
@@ -334,21 +497,15 @@ __global__ __launch_bounds__(WAVES * 64) void router_backward_kernel(RouterArgs 
                 d = kSigmoid ? G * s * rest : s * (G - gs);
             }
         }
+        const double down = total > 0.0 ? -gs / total : 0.0;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            double base = 0.0;
-            if constexpr (kAll)
-                if (x[j] > -__builtin_inff()) base = exp((double)x[j] - (double)top) / total * -gs;
-            row[j * 64 + lane] = base;               // expert lane * EPL + j, kept where this lane reads it
-        }
+        for (int j = 0; j < EPL; ++j)
+            // expert lane * EPL + j, kept where this lane reads it; a masked expert's score is 0, whatever gs
+            row[j * LANES + lane] = kAll && base[kAll ? j : 0] > 0.0 ? base[kAll ? j : 0] * down : 0.0;
         __builtin_amdgcn_wave_barrier();
-        if (named >= 0 && before == 0) row[named % EPL * 64 + named / EPL] = d;
+        if (named >= 0 && before == 0) row[named % EPL * LANES + named / EPL] = d;
         __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const int e = lane * EPL + j;
-            if (e < a.E) write_value(a.dlogits, a.type, (size_t)t * a.E + e, row[j * 64 + lane] * (double)a.scale);
-        }
+        if (real) write_row<EPL>(a.dlogits, a.type, t, a.E, lane, [&](int j) { return row[j * LANES + lane] * (double)a.scale; });
         __builtin_amdgcn_wave_barrier();
     }
 }
@@ -356,7 +513,8 @@ __global__ __launch_bounds__(WAVES * 64) void router_backward_kernel(RouterArgs 
 // ---------------------------------------------------------------- ordering
 struct OrderArgs {
     const int64_t* idx;
-    int32_t *offsets, *order, *slot, *hist;
+    int32_t *offsets, *order, *slot;
+    int32_t* hist;      // [experts][chunks], then [experts] totals
     int pairs, first, experts, chunks, per_chunk;   // per_chunk pairs per work-group
 };
 
@@ -367,55 +525,59 @@ __device__ __forceinline__ int local_of(const OrderArgs& a, int p) {
 
 // Lanes of the wave with the same expert as this one (experts < 4096: 12 bits).
 __device__ __forceinline__ uint64_t same_expert(int e, int bits) {
-    uint64_t m = __ballot(e >= 0);
+    const uint64_t live = __ballot(e >= 0);
+    uint32_t lo = (uint32_t)live, hi = (uint32_t)(live >> 32);
     for (int b = 0; b < bits; ++b) {
         const uint64_t set = __ballot((e >> b) & 1);
-        m &= (e >> b) & 1 ? set : ~set;
+        const uint32_t other = ((uint32_t)e >> b & 1) - 1;          // all ones where this lane's bit is 0
+        lo &= (uint32_t)set ^ other;
+        hi &= (uint32_t)(set >> 32) ^ other;
     }
-    return m;
+    return (uint64_t)hi << 32 | lo;
 }
 
-// Rank the pairs lo .. hi-1 by one wave: `next` (LDS) holds the next free place of every expert.
-__device__ __forceinline__ void place_pairs(const OrderArgs& a, int lo, int hi, int* next, int lane, int bits) {
-    for (int p0 = lo; p0 < hi; p0 += 64) {
-        const int p = p0 + lane;
-        const int e = p < hi ? local_of(a, p) : -1;
-        const uint64_t same = same_expert(e, bits);
-        int place = -1;
-        if (e >= 0) {
-            const int before = __popcll(same & lanemask_lt());
-            const int base = next[e];
-            place = base + before;
-            a.order[place] = p;
-        }
-        __builtin_amdgcn_wave_barrier();
-        if (e >= 0 && (same & lanemask_lt()) == 0) next[e] = place + __popcll(same);
-        __builtin_amdgcn_wave_barrier();
-        if (p < hi) a.slot[p] = place;
+// Places of 64 consecutive pairs, one wave: lane's pair p goes to expert e (-1: none); `next` (LDS, the wave's
+// own) holds the next free place of every expert.
+__device__ __forceinline__ void place_pairs(const OrderArgs& a, int32_t* order, int e, int p, int hi, int* next, int bits) {
+    const uint64_t same = same_expert(e, bits);
+    int place = -1;
+    if (e >= 0) {
+        place = next[e] + __popcll(same & lanemask_lt());
+        order[place] = p;
     }
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0 && (same & lanemask_lt()) == 0) next[e] = place + __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    if (p < hi) a.slot[p] = place;
 }
 
 __device__ __forceinline__ int bits_of(int experts) { return experts > 1 ? 32 - __clz(experts - 1) : 0; }
 
-// Few pairs: everything in one work-group of 16 waves.  Dynamic LDS: int [16][experts], then int [17].
+// Few pairs: everything in one work-group of 16 waves, each with up to 512 consecutive pairs.  The places are put
+// together in LDS and stored in order (8192 pairs, 256 experts: 11 us, against 16 for the three launches below).
+// Dynamic LDS: int [16][experts], int [17 rounded to 32], int [pairs].
 __global__ __launch_bounds__(1024) void order_small_kernel(OrderArgs a) {
     extern __shared__ int lds[];
     int* sums = lds + 16 * a.experts;
+    int* order = sums + 32;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int i = tid; i < 16 * a.experts; i += 1024) lds[i] = 0;
-    __syncthreads();
     const int per = ((a.pairs + 15) / 16 + 63) / 64 * 64;
     const int lo = min(wave * per, a.pairs), hi = min(lo + per, a.pairs);
-    for (int p = lo + lane; p < hi; p += 64) {
-        const int e = local_of(a, p);
-        if (e >= 0) atomicAdd(&lds[wave * a.experts + e], 1);
-    }
+    int mine[kOneGroupPairs / 1024];               // all ids in flight at once
+#pragma unroll
+    for (int i = 0; i < kOneGroupPairs / 1024; ++i) mine[i] = lo + i * 64 + lane < hi ? local_of(a, lo + i * 64 + lane) : -1;
+    for (int i = tid; i < 16 * a.experts; i += 1024) lds[i] = 0;
     __syncthreads();
-    // thread e: the expert's total (experts <= 512), then an exclusive prefix over the experts
+#pragma unroll
+    for (int i = 0; i < kOneGroupPairs / 1024; ++i)
+        if (mine[i] >= 0) atomicAdd(&lds[wave * a.experts + mine[i]], 1);
+    __syncthreads();
+    // thread e: the expert's total (experts <= 256), then an exclusive prefix over the experts
     int count = 0;
     if (tid < a.experts)
+#pragma unroll
         for (int w = 0; w < 16; ++w) count += lds[w * a.experts + tid];
-    int incl = wave_prefix(count, lane);
+    const int incl = wave_prefix(count, lane);
     if (lane == 63) sums[wave] = incl;
     __syncthreads();
     if (wave == 0) {
@@ -428,6 +590,7 @@ __global__ __launch_bounds__(1024) void order_small_kernel(OrderArgs a) {
     if (tid < a.experts) {
         int at = sums[wave] + incl - count;
         a.offsets[tid] = at;
+#pragma unroll
         for (int w = 0; w < 16; ++w) {
             const int c = lds[w * a.experts + tid];
             lds[w * a.experts + tid] = at;
@@ -437,60 +600,49 @@ __global__ __launch_bounds__(1024) void order_small_kernel(OrderArgs a) {
     const int all = sums[16];
     if (tid == 0) a.offsets[a.experts] = all;
     __syncthreads();
-    place_pairs(a, lo, hi, lds + wave * a.experts, lane, bits_of(a.experts));
-    for (int i = all + tid; i < a.pairs; i += 1024) a.order[i] = -1;
+    const int bits = bits_of(a.experts);
+#pragma unroll
+    for (int i = 0; i < kOneGroupPairs / 1024; ++i)
+        if (lo + i * 64 < hi) place_pairs(a, order, mine[i], lo + i * 64 + lane, hi, lds + wave * a.experts, bits);
+    __syncthreads();
+    for (int i = tid; i < a.pairs; i += 1024) a.order[i] = i < all ? order[i] : -1;
 }
 
-// Many pairs, three launches.  1: every chunk's counts, hist[chunk][expert].
+// Many pairs, three launches.  1: every chunk's counts, hist[expert][chunk].  Dynamic LDS: int [experts].
 __global__ __launch_bounds__(256) void order_count_kernel(OrderArgs a) {
     extern __shared__ int lds[];
     for (int i = threadIdx.x; i < a.experts; i += 256) lds[i] = 0;
     __syncthreads();
     const int64_t lo = (int64_t)blockIdx.x * a.per_chunk, hi = min(lo + a.per_chunk, (int64_t)a.pairs);
+#pragma unroll 4
     for (int64_t p = lo + threadIdx.x; p < hi; p += 256) {
         const int e = local_of(a, (int)p);
         if (e >= 0) atomicAdd(&lds[e], 1);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < a.experts; i += 256) a.hist[(size_t)blockIdx.x * a.experts + i] = lds[i];
+    for (int i = threadIdx.x; i < a.experts; i += 256) a.hist[(size_t)i * a.chunks + blockIdx.x] = lds[i];
 }
 
-// 2: hist becomes every chunk's first place within its expert, offsets the experts' first places.  One
-// work-group; thread i handles experts i, i + 1024, ...
-__global__ __launch_bounds__(1024) void order_scan_kernel(OrderArgs a) {
-    __shared__ int sums[17];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int base = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 1024) {
-        const int e = e0 + tid;
-        int count = 0;
-        if (e < a.experts)
-            for (int c = 0; c < a.chunks; ++c) {
-                const size_t i = (size_t)c * a.experts + e;
-                const int v = a.hist[i];
-                a.hist[i] = count;
-                count += v;
-            }
-        const int incl = wave_prefix(count, lane);
-        if (lane == 63) sums[wave] = incl;
-        __syncthreads();
-        if (wave == 0) {
-            const int v = lane < 16 ? sums[lane] : 0;
-            const int s = wave_prefix(v, lane);
-            if (lane < 16) sums[lane] = s - v;
-            if (lane == 15) sums[16] = s;
-        }
-        __syncthreads();
-        if (e < a.experts) a.offsets[e] = base + sums[wave] + incl - count;
-        base += sums[16];
-        __syncthreads();
+// 2: one wave per expert: its chunks' counts become their first places within the expert, and its total.
+__global__ __launch_bounds__(256) void order_scan_kernel(OrderArgs a) {
+    const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (e >= a.experts) return;
+    int32_t* h = a.hist + (size_t)e * a.chunks;
+    int run = 0;
+    for (int c = lane; c - lane < a.chunks; c += 64) {
+        const int v = c < a.chunks ? h[c] : 0;
+        const int incl = wave_prefix(v, lane);
+        if (c < a.chunks) h[c] = run + incl - v;
+        run += __shfl(incl, 63);
     }
-    if (tid == 0) a.offsets[a.experts] = base;
+    if (lane == 0) a.hist[(size_t)a.experts * a.chunks + e] = run;
 }
 
-// 3: places.  Dynamic LDS: int [4][experts].
+// 3: places.  Every work-group adds up the experts' totals for their first places.  Dynamic LDS: int [4][experts],
+// then int [4].
 __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
     extern __shared__ int lds[];
+    int* sums = lds + 4 * a.experts;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t first = (int64_t)blockIdx.x * a.per_chunk;
     const int per = a.per_chunk / 4;
@@ -498,29 +650,52 @@ __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
     const int lo = (int)min(first + (int64_t)wave * per, end), hi = (int)min((int64_t)lo + per, end);
     for (int i = tid; i < 4 * a.experts; i += 256) lds[i] = 0;
     __syncthreads();
+#pragma unroll 4
     for (int p = lo + lane; p < hi; p += 64) {
         const int e = local_of(a, p);
         if (e >= 0) atomicAdd(&lds[wave * a.experts + e], 1);
     }
     __syncthreads();
-    for (int e = tid; e < a.experts; e += 256) {
-        int at = a.offsets[e] + a.hist[(size_t)blockIdx.x * a.experts + e];
+    int base = 0;                                  // pairs of the experts before this batch of 256
+    for (int e0 = 0; e0 < a.experts; e0 += 256) {
+        const int e = e0 + tid;
+        const int before = e < a.experts ? a.hist[(size_t)e * a.chunks + blockIdx.x] : 0;
+        const int count = e < a.experts ? a.hist[(size_t)a.experts * a.chunks + e] : 0;
+        const int incl = wave_prefix(count, lane);
+        if (lane == 63) sums[wave] = incl;
+        __syncthreads();
+        int start = base + incl - count, all = 0;
+#pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const int c = lds[w * a.experts + e];
-            lds[w * a.experts + e] = at;
-            at += c;
+            const int v = sums[w];
+            start += w < wave ? v : 0;
+            all += v;
         }
+        if (e < a.experts) {
+            if (blockIdx.x == 0) a.offsets[e] = start;
+            int at = start + before;
+            for (int w = 0; w < 4; ++w) {
+                const int c = lds[w * a.experts + e];
+                lds[w * a.experts + e] = at;
+                at += c;
+            }
+        }
+        base += all;
+        __syncthreads();
     }
-    __syncthreads();
-    place_pairs(a, lo, hi, lds + wave * a.experts, lane, bits_of(a.experts));
-    for (int64_t i = max(first, (int64_t)a.offsets[a.experts]) + tid; i < end; i += 256) a.order[i] = -1;
+    if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = base;
+    const int bits = bits_of(a.experts);
+    for (int p0 = lo; p0 < hi; p0 += 64)
+        place_pairs(a, a.order, p0 + lane < hi ? local_of(a, p0 + lane) : -1, p0 + lane, hi, lds + wave * a.experts, bits);
+    for (int64_t i = max(first, (int64_t)base) + tid; i < end; i += 256) a.order[i] = -1;
 }
 
-// Pairs per work-group of the three-launch form: a multiple of 4 waves x 64, and at most 1024 chunks for the scan.
-int chunk_pairs(int64_t pairs) {
+// Pairs per work-group of the three-launch form: a multiple of 4 waves x 64, and at most 1024 chunks.
+int64_t chunk_pairs(int64_t pairs) {
     const int64_t least = 4 * kPairsPerWave, by_chunks = (pairs + 1023) / 1024;
-    return (int)((by_chunks < least ? least : by_chunks) + 255) / 256 * 256;
+    return ((by_chunks < least ? least : by_chunks) + 255) / 256 * 256;
 }
+bool one_group(int64_t pairs, int experts) { return pairs <= kOneGroupPairs && experts <= kOneGroupExperts; }
 
 int32_t check_router(const mega_moe_router_config* c) {
     if (!c || c->tokens < 0) return MEGA_MOE_ERR_INVALID_ARG;
@@ -548,41 +723,43 @@ RouterArgs args_of(const mega_moe_router_config* c) {
     return a;
 }
 
-uint32_t router_grid(int64_t tokens, int waves) {
-    const int64_t g = (tokens + waves - 1) / waves;
+uint32_t router_grid(int64_t tokens, int per) {
+    const int64_t g = (tokens + per - 1) / per;
     return (uint32_t)(g < (1 << 20) ? g : 1 << 20);
 }
 
-template <int EPL, bool kSigmoid, bool kWide, bool kGroups>
+template <int EPL, int LANES, bool kSigmoid, bool kWide, bool kGroups>
 hipError_t launch_router(const RouterArgs& a, hipStream_t st) {
     // the groups' values take EPL * 512 bytes of LDS per wave
     constexpr int WAVES = kGroups && EPL > 16 ? 1 : 4;
-    hipLaunchKernelGGL((router_kernel<EPL, kSigmoid, kWide, kGroups, WAVES>), dim3(router_grid(a.tokens, WAVES)),
-                       dim3(WAVES * 64), 0, st, a);
+    hipLaunchKernelGGL((router_kernel<EPL, LANES, kSigmoid, kWide, kGroups, WAVES>),
+                       dim3(router_grid(a.tokens, WAVES * 64 / LANES)), dim3(WAVES * 64), 0, st, a);
     return hipGetLastError();
 }
-template <int EPL>
+template <int EPL, int LANES>
 hipError_t pick_router(const RouterArgs& a, bool sigmoid, hipStream_t st) {
     switch ((sigmoid ? 4 : 0) | (a.bias ? 2 : 0) | (a.G > 1 ? 1 : 0)) {
-        case 0: return launch_router<EPL, false, false, false>(a, st);
-        case 1: return launch_router<EPL, false, false, true>(a, st);
-        case 2: return launch_router<EPL, false, true, false>(a, st);
-        case 3: return launch_router<EPL, false, true, true>(a, st);
-        case 4: return launch_router<EPL, true, false, false>(a, st);
-        case 5: return launch_router<EPL, true, false, true>(a, st);
-        case 6: return launch_router<EPL, true, true, false>(a, st);
-        default: return launch_router<EPL, true, true, true>(a, st);
+        case 0: return launch_router<EPL, LANES, false, false, false>(a, st);
+        case 1: return launch_router<EPL, LANES, false, false, true>(a, st);
+        case 2: return launch_router<EPL, LANES, false, true, false>(a, st);
+        case 3: return launch_router<EPL, LANES, false, true, true>(a, st);
+        case 4: return launch_router<EPL, LANES, true, false, false>(a, st);
+        case 5: return launch_router<EPL, LANES, true, false, true>(a, st);
+        case 6: return launch_router<EPL, LANES, true, true, false>(a, st);
+        default: return launch_router<EPL, LANES, true, true, true>(a, st);
     }
 }
-template <int EPL>
+template <int EPL, int LANES>
 hipError_t pick_backward(const RouterArgs& a, bool sigmoid, hipStream_t st) {
     constexpr int WAVES = EPL > 16 ? 1 : 4;
-    const dim3 grid(router_grid(a.tokens, WAVES)), block(WAVES * 64);
-    if (sigmoid) hipLaunchKernelGGL((router_backward_kernel<EPL, true, false, WAVES>), grid, block, 0, st, a);
-    else if (a.renorm) hipLaunchKernelGGL((router_backward_kernel<EPL, false, false, WAVES>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((router_backward_kernel<EPL, false, true, WAVES>), grid, block, 0, st, a);
+    const dim3 grid(router_grid(a.tokens, WAVES * 64 / LANES)), block(WAVES * 64);
+    if (sigmoid) hipLaunchKernelGGL((router_backward_kernel<EPL, LANES, true, false, WAVES>), grid, block, 0, st, a);
+    else if (a.renorm) hipLaunchKernelGGL((router_backward_kernel<EPL, LANES, false, false, WAVES>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((router_backward_kernel<EPL, LANES, false, true, WAVES>), grid, block, 0, st, a);
     return hipGetLastError();
 }
+// A quarter wave per token: enough tokens to fill the CUs with them (4 waves to a SIMD), and room in 16 lanes.
+bool by_quarters(const RouterArgs& a) { return a.tokens >= 4096 && a.E <= 256 && a.K <= 16 && a.G <= 16; }
 
 bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
 
@@ -607,12 +784,15 @@ int32_t mega_moe_router_topk(const mega_moe_router_config* cfg, const void* logi
     a.weights = topk_weights;
     const bool sigmoid = cfg->score == MEGA_MOE_SCORE_SIGMOID;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const hipError_t e = a.E <= 64     ? pick_router<1>(a, sigmoid, st)
-                         : a.E <= 128  ? pick_router<2>(a, sigmoid, st)
-                         : a.E <= 256  ? pick_router<4>(a, sigmoid, st)
-                         : a.E <= 512  ? pick_router<8>(a, sigmoid, st)
-                         : a.E <= 1024 ? pick_router<16>(a, sigmoid, st)
-                                       : pick_router<64>(a, sigmoid, st);
+    const hipError_t e = by_quarters(a) ? (a.E <= 64    ? pick_router<4, 16>(a, sigmoid, st)
+                                           : a.E <= 128 ? pick_router<8, 16>(a, sigmoid, st)
+                                                        : pick_router<16, 16>(a, sigmoid, st))
+                         : a.E <= 64   ? pick_router<1, 64>(a, sigmoid, st)
+                         : a.E <= 128  ? pick_router<2, 64>(a, sigmoid, st)
+                         : a.E <= 256  ? pick_router<4, 64>(a, sigmoid, st)
+                         : a.E <= 512  ? pick_router<8, 64>(a, sigmoid, st)
+                         : a.E <= 1024 ? pick_router<16, 64>(a, sigmoid, st)
+                                       : pick_router<64, 64>(a, sigmoid, st);
     return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
@@ -630,12 +810,15 @@ int32_t mega_moe_router_backward(const mega_moe_router_config* cfg, const float*
     a.dlogits = dlogits;
     const bool sigmoid = cfg->score == MEGA_MOE_SCORE_SIGMOID;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const hipError_t e = a.E <= 64     ? pick_backward<1>(a, sigmoid, st)
-                         : a.E <= 128  ? pick_backward<2>(a, sigmoid, st)
-                         : a.E <= 256  ? pick_backward<4>(a, sigmoid, st)
-                         : a.E <= 512  ? pick_backward<8>(a, sigmoid, st)
-                         : a.E <= 1024 ? pick_backward<16>(a, sigmoid, st)
-                                       : pick_backward<64>(a, sigmoid, st);
+    const hipError_t e = by_quarters(a) ? (a.E <= 64    ? pick_backward<4, 16>(a, sigmoid, st)
+                                           : a.E <= 128 ? pick_backward<8, 16>(a, sigmoid, st)
+                                                        : pick_backward<16, 16>(a, sigmoid, st))
+                         : a.E <= 64   ? pick_backward<1, 64>(a, sigmoid, st)
+                         : a.E <= 128  ? pick_backward<2, 64>(a, sigmoid, st)
+                         : a.E <= 256  ? pick_backward<4, 64>(a, sigmoid, st)
+                         : a.E <= 512  ? pick_backward<8, 64>(a, sigmoid, st)
+                         : a.E <= 1024 ? pick_backward<16, 64>(a, sigmoid, st)
+                                       : pick_backward<64, 64>(a, sigmoid, st);
     return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
@@ -644,7 +827,7 @@ int32_t mega_moe_group_workspace_bytes(int64_t pairs, int32_t num_local_experts,
     if (pairs >= (int64_t)1 << 31 || num_local_experts < 1 || num_local_experts > MEGA_MOE_MAX_EXPERTS)
         return MEGA_MOE_ERR_UNSUPPORTED;
     const int64_t per = chunk_pairs(pairs);
-    *bytes_out = (uint64_t)((pairs + per - 1) / per + 1) * num_local_experts * 4;
+    *bytes_out = one_group(pairs, num_local_experts) ? 0 : (uint64_t)((pairs + per - 1) / per + 1) * num_local_experts * 4;
     return MEGA_MOE_OK;
 }
 
@@ -655,23 +838,24 @@ int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t
     const int32_t rc = mega_moe_group_workspace_bytes(pairs, num_local_experts, &need);
     if (rc) return rc;
     if (first_expert < 0) return MEGA_MOE_ERR_INVALID_ARG;
-    if (!aligned16(offsets) || !aligned16(workspace) ||
+    if (!aligned16(offsets) || (need && !aligned16(workspace)) ||
         (pairs > 0 && (!aligned16(topk_idx) || !aligned16(order) || !aligned16(slot))))
         return MEGA_MOE_ERR_INVALID_ARG;
     if (workspace_bytes < need) return MEGA_MOE_ERR_WORKSPACE_TOO_SMALL;
     hipStream_t st = static_cast<hipStream_t>(stream);
     OrderArgs a{topk_idx, offsets, order, slot, static_cast<int32_t*>(workspace), (int)pairs, first_expert,
                 num_local_experts, 0, 0};
-    if (pairs <= kOneGroupPairs && num_local_experts <= kOneGroupExperts) {
-        hipLaunchKernelGGL(order_small_kernel, dim3(1), dim3(1024), (16 * num_local_experts + 17) * sizeof(int), st, a);
+    if (one_group(pairs, num_local_experts)) {
+        hipLaunchKernelGGL(order_small_kernel, dim3(1), dim3(1024), (16 * num_local_experts + 32 + pairs) * sizeof(int), st, a);
         return hipGetLastError() == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
     }
-    a.per_chunk = chunk_pairs(pairs);
+    a.per_chunk = (int)chunk_pairs(pairs);
     a.chunks = (int)((pairs + a.per_chunk - 1) / a.per_chunk);
-    const dim3 chunks(a.chunks > 0 ? a.chunks : 1), block(256);
+    if (a.chunks == 0) a.chunks = 1;
+    const dim3 chunks(a.chunks), block(256);
     hipLaunchKernelGGL(order_count_kernel, chunks, block, num_local_experts * sizeof(int), st, a);
-    hipLaunchKernelGGL(order_scan_kernel, dim3(1), dim3(1024), 0, st, a);
-    hipLaunchKernelGGL(order_place_kernel, chunks, block, 4 * num_local_experts * sizeof(int), st, a);
+    hipLaunchKernelGGL(order_scan_kernel, dim3((num_local_experts + 3) / 4), block, 0, st, a);
+    hipLaunchKernelGGL(order_place_kernel, chunks, block, (4 * num_local_experts + 4) * sizeof(int), st, a);
     return hipGetLastError() == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 

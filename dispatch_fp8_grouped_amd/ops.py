@@ -148,8 +148,8 @@ class _Call:
         if stream is None:
             if torch._C._cuda_getDevice() != device.index:
                 self.ctx = torch.cuda.device(device)
-            # the handle of torch.cuda.current_stream(device), without making the object: a call's whole host
-            # time went from 12 to 6 us with it, and small calls are bound by that
+            # the handle of torch.cuda.current_stream(device), without making the object: the host time
+            # of a call went from 12.4 to 8.6 us with it, and small calls are bound by that
             self.raw = torch._C._cuda_getCurrentRawStream(device.index)
         else:
             if isinstance(stream, int):
@@ -305,7 +305,7 @@ def group_by_expert(topk_idx, num_local_experts, first_expert=0, stream=None):
         offsets = torch.empty(num_local_experts + 1, dtype=torch.int32, device=device)
         order = torch.empty(pairs, dtype=torch.int32, device=device)
         slot = torch.empty(topk_idx.shape, dtype=torch.int32, device=device)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
         mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, offsets, order, slot, workspace,
                                  nbytes, raw)
     return offsets, order, slot

@@ -119,7 +119,7 @@ int32_t mega_moe_router_backward(const mega_moe_router_config* cfg, const float*
  *   order      int32 [pairs]: order[i] = pair at place i; pairs of one expert in increasing order; -1 from
  *              offsets[num_local_experts] on
  *   slot       int32 [pairs]: the place of pair p, -1 if it belongs to no group here
- *   workspace  mega_moe_group_workspace_bytes() bytes; its contents do not matter
+ *   workspace  mega_moe_group_workspace_bytes() bytes (may be NULL at 0); its contents do not matter
  * pairs 0 .. 2^31-1 (pointers of pair arrays may be NULL at 0); num_local_experts 1 .. MEGA_MOE_MAX_EXPERTS.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP. */
 int32_t mega_moe_group_workspace_bytes(int64_t pairs, int32_t num_local_experts, uint64_t* bytes_out /* host */);

@@ -61,14 +61,15 @@ def route_row(row, k, bias, score, groups, kept, group_top, renorm, scale):
     return idx + [-1] * pad, [v * scale for v in w] + [0.0] * pad
 
 
-def check_forward(logits, k, bias=None, score="softmax", groups=1, kept=1, group_top=1, renorm=True, scale=1.0):
+def check_forward(logits, k, bias=None, score="softmax", groups=1, kept=1, group_top=1, renorm=True, scale=1.0,
+                  rows=slice(None)):
     idx, w = mm.router_topk(logits, k, bias=bias, score=score, num_groups=groups, topk_groups=kept, group_top=group_top,
                             renormalize=renorm, scale=scale)
     assert idx.dtype == torch.int64 and w.dtype == torch.float32
-    rows = logits.double().cpu().tolist()
+    sample, i_s, w_s = logits[rows].double().cpu().tolist(), idx[rows], w[rows]
     b = None if bias is None else bias.double().cpu().tolist()
-    want = [route_row(r, k, b, score, groups, kept, group_top, renorm, scale) for r in rows]
-    got_i, got_w = idx.cpu().tolist(), w.double().cpu().numpy()
+    want = [route_row(r, k, b, score, groups, kept, group_top, renorm, scale) for r in sample]
+    got_i, got_w = i_s.cpu().tolist(), w_s.double().cpu().numpy()
     for t, (wi, ww) in enumerate(want):
         assert got_i[t] == wi, (t, got_i[t], wi)
     ww = np.array([x[1] for x in want], dtype=np.float64).reshape(got_w.shape)
@@ -101,6 +102,33 @@ def test_choice_and_weights(t, e, k, groups, kept, kind, score):
         check_forward(x, k, None, score, groups, kept, 2, renorm)
         check_forward(x, k, bias, score, groups, kept, 1, renorm)
         check_forward(x, k, None, score, groups, kept, 1, renorm, 0.5)
+
+
+# many tokens: a quarter wave each.  The last tokens of a wave and of a work-group are missing
+MANY = [(4097, 7, 7, 1, 1), (4099, 60, 6, 5, 2), (5000, 64, 16, 16, 3), (4110, 100, 4, 4, 2), (6001, 128, 8, 8, 3),
+        (4096, 200, 12, 1, 1), (9001, 256, 8, 8, 4)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("t,e,k,groups,kept", MANY)
+def test_many_tokens(t, e, k, groups, kept, kind, score):
+    print(f"[case] {t} {e} {k} {groups} {kept} {kind} {score}", flush=True)
+    x = logits_of(t, e, kind, seed=e + 5)
+    x[3] = float("-inf")
+    x[t - 2, ::2] = float("nan")
+    x[t - 1] = 0.5
+    rows = torch.tensor([*range(12), *range(t // 2, t // 2 + 9), *range(t - 25, t)], device="cuda")
+    bias = torch.randn(e, device="cuda", generator=torch.Generator(device="cuda").manual_seed(e)) * 0.1
+    g = torch.randn(t, k, device="cuda", generator=torch.Generator(device="cuda").manual_seed(9))
+    for renorm in (True, False):
+        check_forward(x, k, None, score, 1, 1, 1, renorm, rows=rows)
+        check_forward(x, k, bias, score, groups, kept, 2, renorm, 2.5, rows=rows)
+        check_forward(x, k, bias, score, 1, 1, 1, renorm, rows=rows)
+        idx, _ = check_forward(x, k, None, score, groups, kept, 2, renorm, rows=rows)
+        idx[4, 0] = -1
+        idx[5, k - 1] = idx[5, 0]
+        check_backward(x, idx, g, score, renorm, 2.5, sel=rows)
 
 
 def test_ties_go_to_the_lowest_expert():
@@ -178,11 +206,12 @@ def reference_backward(g, row, idx, score, renorm, scale):
     return [v * (d - dot) if v else 0.0 for d, v in zip(ds, s)], [v * (m + amp) for m, v in zip(mag, s)]
 
 
-def check_backward(logits, idx, g, score, renorm, scale=1.0):
+def check_backward(logits, idx, g, score, renorm, scale=1.0, sel=slice(None)):
     d = mm.router_backward(g, logits, idx, score=score, renormalize=renorm, scale=scale)
     assert d.dtype == logits.dtype and d.shape == logits.shape
-    rows, ids, gs = logits.double().cpu().tolist(), idx.cpu().tolist(), g.double().cpu().tolist()
-    got, eps = d.double().cpu().numpy(), torch.finfo(logits.dtype).eps
+    rows, ids, gs = (v[sel].double().cpu().tolist() for v in (logits, idx, g))
+    ids = [[int(e) for e in r] for r in ids]
+    got, eps = d[sel].double().cpu().numpy(), torch.finfo(logits.dtype).eps
     tiny = torch.finfo(logits.dtype).smallest_normal * eps
     for t in range(len(rows)):
         want, mag = map(np.array, reference_backward(gs[t], rows[t], ids[t], score, renorm, scale))

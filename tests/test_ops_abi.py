@@ -107,7 +107,7 @@ def test_ordering_refusals():
     for i in range(5):
         args = [P] * 5
         args[i] = ODD
-        a = (args[0], 10, 0, 4, *args[1:])
+        a = (args[0], 100000, 0, 256, *args[1:])
         assert lib.mega_moe_group_by_expert(*a, need, None) == mm.ERR_INVALID_ARG, i
 
 
