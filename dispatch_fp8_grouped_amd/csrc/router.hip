@@ -240,7 +240,8 @@ __device__ __forceinline__ void merge_top2(double& a, double& b, double c, doubl
     a = hi;
 }
 
-// kWide: 64-bit ranks (a bias is given).  A work-group's tokens follow each other.
+// kWide: ranks as two words (with a bias, or with too many experts to a lane to sort).  A work-group's tokens
+// follow each other.
 template <int EPL, int LANES, bool kSigmoid, bool kWide, bool kGroups, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1) void router_kernel(RouterArgs a) {
     constexpr int kTokens = WAVES * 64 / LANES;
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1
         }
         // softmax needs its largest logit and its sum where the scores themselves enter the result; where they
         // are divided by the chosen ones' sum both cancel
-        const bool by_score = kWide || (kGroups && a.gtop == 2);
+        const bool by_score = (kWide && a.bias) || (kGroups && a.gtop == 2);
         double total = 1.0;
         if (!kSigmoid && (by_score || !a.renorm)) {
             top = max_of<LANES>(top);              // -inf where everything is masked
@@ -282,7 +283,7 @@ __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1
             if (by_score && live[j]) {
                 const double s = kSigmoid ? sigmoid64(x[j]) : exp((double)x[j] - (double)top) / total;
                 worth = s;
-                if constexpr (kWide) {
+                if (kWide && a.bias) {
                     worth = rank = s + (double)a.bias[e];
                     live[j] = rank > none;         // not -inf, not NaN
                 }
@@ -369,18 +370,6 @@ __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1
         } else {
             // every lane's experts sorted once: a round looks at the lanes' first ones, and the lane that had the
             // largest moves up.  Only the first K of a lane can be reached.
-            if constexpr (EPL > 16) {
-                // too many to sort in registers: every round walks them
-                for (int k = 0; k < a.K; ++k) {
-                    double first = none;
-#pragma unroll
-                    for (int j = 0; j < EPL; ++j) first = fmax(first, key[j]);
-                    const double best = max_of<LANES>(first);
-                    if (lane == k && best > none) chosen = expert_of(best);
-#pragma unroll
-                    for (int j = 0; j < EPL; ++j) key[j] = key[j] == best ? none : key[j];
-                }
-            } else {
             sort_down(key);
             auto rounds = [&](auto depth) {
                 constexpr int kDepth = decltype(depth)::value;
@@ -394,7 +383,6 @@ __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1
             };
             if (EPL > 8 && a.K <= 8) rounds(std::integral_constant<int, EPL < 8 ? EPL : 8>{});
             else rounds(std::integral_constant<int, EPL>{});
-            }
         }
         // the chosen logit once more, from the cache
         float chosen_x = chosen >= 0 ? clip_inf(read_value(a.logits, a.type, (size_t)t * a.E + chosen)) : -__builtin_inff();
@@ -738,13 +726,14 @@ hipError_t launch_router(const RouterArgs& a, hipStream_t st) {
 }
 template <int EPL, int LANES>
 hipError_t pick_router(const RouterArgs& a, bool sigmoid, hipStream_t st) {
-    switch ((sigmoid ? 4 : 0) | (a.bias ? 2 : 0) | (a.G > 1 ? 1 : 0)) {
-        case 0: return launch_router<EPL, LANES, false, false, false>(a, st);
-        case 1: return launch_router<EPL, LANES, false, false, true>(a, st);
+    constexpr bool kWalk = EPL > 16;               // always as words
+    switch ((sigmoid ? 4 : 0) | (a.bias || kWalk ? 2 : 0) | (a.G > 1 ? 1 : 0)) {
+        case 0: return launch_router<EPL, LANES, false, kWalk, false>(a, st);
+        case 1: return launch_router<EPL, LANES, false, kWalk, true>(a, st);
         case 2: return launch_router<EPL, LANES, false, true, false>(a, st);
         case 3: return launch_router<EPL, LANES, false, true, true>(a, st);
-        case 4: return launch_router<EPL, LANES, true, false, false>(a, st);
-        case 5: return launch_router<EPL, LANES, true, false, true>(a, st);
+        case 4: return launch_router<EPL, LANES, true, kWalk, false>(a, st);
+        case 5: return launch_router<EPL, LANES, true, kWalk, true>(a, st);
         case 6: return launch_router<EPL, LANES, true, true, false>(a, st);
         default: return launch_router<EPL, LANES, true, true, true>(a, st);
     }
