@@ -18,7 +18,7 @@ namespace mm {
 template <class T, bool kPKs, bool kQKs, int BM, int BN, int WM, int WN, int NST>
 struct TileLoop {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-    static constexpr int MI = BM / 16 / WM, QI = BN / 16 / WN;
+    static constexpr int kRows = BM, MI = BM / 16 / WM, QI = BN / 16 / WN;
     static constexpr int kPBytes = BM * 128, kStage = (BM + BN) * 128, kLds = NST * kStage;
     static constexpr int kPInstr = BM / 8 / kWaves, kQInstr = BN / 8 / kWaves, kInstr = kPInstr + kQInstr;
 
@@ -120,7 +120,7 @@ struct TileLoop {
 template <class T, bool kPKs, bool kQKs, int BM, int BN, int WM, int WN>
 struct QuadLoop {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
-    static constexpr int MI = BM / 16 / WM, QI = BN / 16 / WN, MH = MI / 2, QH = QI / 2;
+    static constexpr int kRows = BM, MI = BM / 16 / WM, QI = BN / 16 / WN, MH = MI / 2, QH = QI / 2;
     static constexpr int kPHalf = BM / 2 * 128, kQHalf = BN / 2 * 128, kLds = 4 * (kPHalf + kQHalf);
     static constexpr int kPInstr = BM / 16 / kWaves, kQInstr = BN / 16 / kWaves, kInstr = kPInstr + kQInstr;
     static constexpr int kQuad = MH * QH * 2;                 // MFMAs of a quadrant

@@ -58,7 +58,7 @@ def _bind(L):
     L.mega_moe_router_backward.argtypes = [cfg, vp, vp, vp, vp, vp]
     L.mega_moe_group_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(u64)]
     L.mega_moe_group_by_expert.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, u64, vp]
-    L.mega_moe_adapter_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(u64)]
+    L.mega_moe_adapter_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, ctypes.POINTER(u64)]
     L.mega_moe_adapter_forward.argtypes = [vp] * 8 + [i64] + [i32] * 6 + [vp, u64, vp, vp]
     for name in OPS_EXPORTS:
         getattr(L, name).restype = i32
@@ -110,9 +110,10 @@ def mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, o
                                                 nbytes, _mm._stream(stream)), "mega_moe_group_by_expert")
 
 
-def mega_moe_adapter_workspace_bytes(rows: int, rank: int) -> int:
+def mega_moe_adapter_workspace_bytes(rows: int, n: int, k: int, rank: int, requests: int) -> int:
     out = ctypes.c_uint64(0)
-    _mm._check(_mm.lib().mega_moe_adapter_workspace_bytes(rows, rank, ctypes.byref(out)), "mega_moe_adapter_workspace_bytes")
+    _mm._check(_mm.lib().mega_moe_adapter_workspace_bytes(rows, n, k, rank, requests, ctypes.byref(out)),
+               "mega_moe_adapter_workspace_bytes")
     return out.value
 
 
@@ -332,7 +333,7 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
         _want(name, t, shape, types, w.device)
     if status is not None:
         _want("status", status, (1,), (torch.int32,), w.device)
-    nbytes = mega_moe_adapter_workspace_bytes(rows, rank)
+    nbytes = mega_moe_adapter_workspace_bytes(rows, n, k, rank, requests)
     with _Call(w.device, stream) as raw:
         if out is None:
             out = torch.empty((rows, n), dtype=w.dtype, device=w.device)

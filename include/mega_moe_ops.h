@@ -143,7 +143,8 @@ int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t
  * the sum of two 16-bit numbers, the value rounded and the rounded remainder.  In fp16 it has fp16's range:
  * beyond 65504 it is infinite, below 6e-8 it is 0.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP. */
-int32_t mega_moe_adapter_workspace_bytes(int64_t rows, int32_t rank, uint64_t* bytes_out /* host */);
+int32_t mega_moe_adapter_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t rank, int32_t requests,
+                                         uint64_t* bytes_out /* host */);
 int32_t mega_moe_adapter_forward(const void* x, const void* w, const void* a, const void* b, const float* scales,
                                  const int32_t* offsets, const int32_t* adapter, void* y, int64_t rows, int32_t n,
                                  int32_t k, int32_t rank, int32_t requests, int32_t adapters, int32_t dtype,

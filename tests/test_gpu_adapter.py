@@ -60,6 +60,12 @@ CASES = [
     ([0, 130, 131, 400], [0, 1, 2], 400, 72, 1032, 256, 3),
     ([0], [], 50, 136, 72, 8, 1),                                        # no request at all
     ([0, 17, 34, 51], [-1, -1, -1], 51, 136, 72, 8, 1),
+    ([0, 1], [1], 1, 2056, 2048, 48, 2),                                 # long contractions, split between work-groups
+    ([0, 3, 60, 61], [0, 1, 1], 61, 1032, 4104, 128, 2),
+    ([0, 255], [0], 256, 392, 1544, 16, 1),
+    ([0, 250, 257], [0, 1], 257, 392, 1544, 16, 2),                      # just too many rows for that
+    ([0, 1000, 1001, 5000, 5100], [0, 1, 2, 0], 5131, 2056, 520, 24, 3),  # the large tiles
+    ([0, 4000, 9000], [1, 0], 9000, 4104, 136, 72, 2),
 ]
 
 
@@ -96,7 +102,7 @@ def test_one_requests_infinities_reach_no_other_row():
 def test_workspace_contents_do_not_matter_and_out_is_used():
     s = make([0, 9, 30, 64], [1, -1, 0], 70, 136, 136, 24, 2, torch.float16, seed=23)
     want = mm.adapter_forward(**s)
-    ws = torch.full((mm.mega_moe_adapter_workspace_bytes(70, 24),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((mm.mega_moe_adapter_workspace_bytes(70, 136, 136, 24, 3),), 0xFF, dtype=torch.uint8, device="cuda")
     y = torch.full_like(want, float("nan"))
     assert mm.adapter_forward(**s, out=y, workspace=ws) is y
     assert torch.equal(y, want)

@@ -135,13 +135,13 @@ def test_adapter_refusals():
     for kw in (dict(rank=0), dict(rank=12), dict(rank=264), dict(n=12), dict(k=20), dict(n=65544), dict(adapters=0),
                dict(adapters=65537), dict(requests=4097), dict(dtype=mm.FP32), dict(rows=(1 << 26) + 1)):
         assert adapter_call(**kw) == mm.ERR_UNSUPPORTED, kw
-    assert adapter_call(nbytes=mm.mega_moe_adapter_workspace_bytes(4, 8) - 1) == mm.ERR_WORKSPACE_TOO_SMALL
+    assert adapter_call(nbytes=mm.mega_moe_adapter_workspace_bytes(4, 16, 16, 8, 2) - 1) == mm.ERR_WORKSPACE_TOO_SMALL
     assert adapter_call(rows=0, x=None, y=None) == mm.OK
     out = ctypes.c_uint64(0)
     lib = mm.lib()
-    assert lib.mega_moe_adapter_workspace_bytes(4, 8, None) == mm.ERR_INVALID_ARG
-    assert lib.mega_moe_adapter_workspace_bytes(-1, 8, ctypes.byref(out)) == mm.ERR_INVALID_ARG
-    assert lib.mega_moe_adapter_workspace_bytes(4, 12, ctypes.byref(out)) == mm.ERR_UNSUPPORTED
+    assert lib.mega_moe_adapter_workspace_bytes(4, 16, 16, 8, 2, None) == mm.ERR_INVALID_ARG
+    assert lib.mega_moe_adapter_workspace_bytes(-1, 16, 16, 8, 2, ctypes.byref(out)) == mm.ERR_INVALID_ARG
+    assert lib.mega_moe_adapter_workspace_bytes(4, 16, 16, 12, 2, ctypes.byref(out)) == mm.ERR_UNSUPPORTED
     x = torch.zeros(4, 16)
     with pytest.raises(ValueError):
         mm.adapter_forward(x, x, x, x, x, x, x)
