@@ -308,13 +308,15 @@ struct Plan {
 Plan plan_of(int rows, int n, int k, int rank, int requests) {
     Plan p{};
     const int steps = (k + kStepK - 1) / kStepK;
+    p.few = rows <= kFewRows;
     const auto split = [&](int64_t tiles, int most, int& parts, int& per) {
-        // two work-groups to a CU, and at least four steps to a part (its pipeline is three deep)
-        parts = clamp(512 / (tiles > 0 ? tiles : 1), 1, clamp(steps / 4, 1, most));
+        // a work-group to a CU where the launch has others beside them, else two (64 requests, 4096 x 7168: 30 us
+        // against 34 the other way, parts and joining launch together), and at least four steps to a part, whose
+        // pipeline is three deep
+        parts = clamp((p.few ? 256 : 512) / (tiles > 0 ? tiles : 1), 1, clamp(steps / 4, 1, most));
         per = (steps + parts - 1) / parts;
         parts = (steps + per - 1) / per;
     };
-    p.few = rows <= kFewRows;
     p.u_tiles = requests > 0 ? ((int64_t)rows / kDownM + (requests < rows ? requests : rows)) * ((rank + kDownN - 1) / kDownN) : 0;
     split(p.u_tiles, 8, p.u_parts, p.u_steps);
     p.y_tiles = (int64_t)((rows + kPartM - 1) / kPartM) * ((n + kPartN - 1) / kPartN);

@@ -15,15 +15,20 @@
 
 namespace mm {
 
-template <class T, bool kPKs, bool kQKs, int BM, int BN, int WM, int WN, int NST>
+//
+// G > 1: G groups of waves take every G-th step, each in LDS stages of its own, and group 0 adds up their
+// accumulators at the end.  For products with few tiles: the same tile with G times the bytes in flight and a
+// G-th of the steps one after the other.
+template <class T, bool kPKs, bool kQKs, int BM, int BN, int WM, int WN, int NST, int G = 1>
 struct TileLoop {
-    static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
+    static constexpr int kGroup = WM * WN, kWaves = kGroup * G, kThreads = kWaves * 64;
     static constexpr int kRows = BM, MI = BM / 16 / WM, QI = BN / 16 / WN;
-    static constexpr int kPBytes = BM * 128, kStage = (BM + BN) * 128, kLds = NST * kStage;
-    static constexpr int kPInstr = BM / 8 / kWaves, kQInstr = BN / 8 / kWaves, kInstr = kPInstr + kQInstr;
+    static constexpr int kPBytes = BM * 128, kStage = (BM + BN) * 128;
+    static constexpr int kStages = NST * G * kStage, kSums = (G - 1) * BM * BN * 4, kLds = kStages > kSums ? kStages : kSums;
+    static constexpr int kPInstr = BM / 8 / kGroup, kQInstr = BN / 8 / kGroup, kInstr = kPInstr + kQInstr;
 
     // Tile row of accumulator column j, tile column of accumulator row i (first of 16)
-    static __device__ __forceinline__ int row(int wave, int j) { return (wave / WN * MI + j) * 16; }
+    static __device__ __forceinline__ int row(int wave, int j) { return (wave / WN % WM * MI + j) * 16; }
     static __device__ __forceinline__ int col(int wave, int i) { return (wave % WN * QI + i) * 16; }
     using Acc = f32x4;
     static constexpr int kRun = QI;       // accumulator rows i whose columns follow each other in the tile
@@ -64,49 +69,69 @@ struct TileLoop {
         }
         __builtin_amdgcn_sched_barrier(0);
     }
+    // Whether this wave holds the tile's sums after run()
+    static __device__ __forceinline__ bool owns(int wave) { return wave < kGroup; }
     // All waves take part; acc is overwritten.
     static __device__ __forceinline__ void run(const Operand& po, const Operand& qo, uint8_t* smem, int wave, int lane,
                                                f32x4 (&acc)[QI][MI]) {
-        const auto P = PartOf<kPKs, BM, kWaves>::make(po, 0, wave, lane);
-        const auto Q = PartOf<kQKs, BN, kWaves>::make(qo, 0, wave, lane);
-        const int steps = (po.len + kStepK - 1) / kStepK, wm = wave / WN, wn = wave % WN;
-        const uint32_t lds = lds_byte(smem);
+        const int group = wave / kGroup, member = wave % kGroup;
+        const auto P = PartOf<kPKs, BM, kGroup>::make(po, 0, member, lane);
+        const auto Q = PartOf<kQKs, BN, kGroup>::make(qo, 0, member, lane);
+        const int steps = (po.len + G * kStepK - 1) / (G * kStepK), wm = member / WN, wn = member % WN;
+        uint8_t* stages = smem + group * NST * kStage;
+        const uint32_t lds = lds_byte(stages);
 #pragma unroll
         for (int i = 0; i < QI; ++i)
 #pragma unroll
             for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < NST; ++s) {
-            const auto ps = P.step(s);
-            const auto qs = Q.step(s);
+            const auto ps = P.step(s * G + group);
+            const auto qs = Q.step(s * G + group);
 #pragma unroll
-            for (int j = 0; j < kPInstr; ++j) P.load(ps, j, lds + s * kStage, wave);
+            for (int j = 0; j < kPInstr; ++j) P.load(ps, j, lds + s * kStage, member);
 #pragma unroll
-            for (int j = 0; j < kQInstr; ++j) Q.load(qs, j, lds + s * kStage + kPBytes, wave);
+            for (int j = 0; j < kQInstr; ++j) Q.load(qs, j, lds + s * kStage + kPBytes, member);
         }
         i32x4 p0[MI], q0[QI], p1[MI], q1[QI];
         wait_vm_barrier<(NST - 1) * kInstr>();
 #pragma unroll
-        for (int r = 0; r < QI + MI; ++r) read(r, smem, 0, wm, wn, lane, p0, q0);
+        for (int r = 0; r < QI + MI; ++r) read(r, stages, 0, wm, wn, lane, p0, q0);
         int cur = 0;
         for (int s = 0; s < steps; ++s) {
             const int nxt = cur + 1 == NST ? 0 : cur + 1;
-            const uint8_t *here = smem + cur * kStage, *next = smem + nxt * kStage;
+            const uint8_t *here = stages + cur * kStage, *next = stages + nxt * kStage;
             multiply<QI + MI, 0>(p0, q0, acc, [&](int r) { read(r, here, 1, wm, wn, lane, p1, q1); }, [](int) {});
             wait_vm_barrier<(NST - 2) * kInstr>();
             __builtin_amdgcn_sched_barrier(0);
-            const auto ps = P.step(s + NST);
-            const auto qs = Q.step(s + NST);
+            const auto ps = P.step((s + NST) * G + group);
+            const auto qs = Q.step((s + NST) * G + group);
             const uint32_t to = lds + cur * kStage;
             multiply<QI + MI, kInstr>(p1, q1, acc, [&](int r) { read(r, next, 0, wm, wn, lane, p0, q0); },
                                       [&](int d) {
-                                          if (d < kPInstr) P.load(ps, d, to, wave);
-                                          else Q.load(qs, d - kPInstr, to + kPBytes, wave);
+                                          if (d < kPInstr) P.load(ps, d, to, member);
+                                          else Q.load(qs, d - kPInstr, to + kPBytes, member);
                                       });
             cur = nxt;
         }
         // the loads past the end still write zeros to LDS: nothing may outlive the work-group or meet a reuse
         wait_vm_barrier<0>();
+        if constexpr (G > 1) {
+            f32x4* sums = reinterpret_cast<f32x4*>(smem) + (size_t)member * QI * MI * 64 + lane;
+            constexpr int kNext = kGroup * QI * MI * 64;
+            if (group > 0) {
+#pragma unroll
+                for (int i = 0; i < QI * MI; ++i) sums[(group - 1) * kNext + i * 64] = acc[i / MI][i % MI];
+            }
+            wait_vm_barrier<0>();
+            if (group == 0) {
+#pragma unroll
+                for (int g = 0; g < G - 1; ++g)
+#pragma unroll
+                    for (int i = 0; i < QI * MI; ++i) acc[i / MI][i % MI] += sums[g * kNext + i * 64];
+            }
+            wait_vm_barrier<0>();
+        }
     }
 };
 
@@ -175,6 +200,7 @@ struct QuadLoop {
         }
         __builtin_amdgcn_sched_barrier(0);
     }
+    static __device__ __forceinline__ bool owns(int) { return true; }
     // All waves take part; acc is overwritten.
     static __device__ __forceinline__ void run(const Operand& po, const Operand& qo, uint8_t* smem, int wave, int lane,
                                                f32x4 (&acc)[QI][MI]) {
@@ -253,6 +279,7 @@ __device__ __forceinline__ void store_tile(const typename L::Acc (&acc)[L::QI][L
     constexpr int kShare = L::kLds / L::kWaves / 16 * 16, kSlots = kShare / kBlock;
     static_assert(kSlots >= 1, "a block of rows fits a wave's share of LDS");
     constexpr int kChunks = kRow / 16, kPer = 16 / kBytes;        // 16-byte chunks of a row, values of a chunk
+    if (!L::owns(wave)) return;
     uint8_t* mine = smem + wave * kShare;
 #pragma unroll
     for (int j = 0; j < L::MI; ++j)
@@ -286,18 +313,22 @@ __device__ __forceinline__ void store_halves(const typename L::Acc (&acc)[L::QI]
 // Which tile shape a row product of these sizes runs with (forward and backward of the groups, the adapters'
 // shared product).  The time is estimated as `fixed` + steps * (a tile's time per step) * (rounds of tiles over the
 // CUs), with the microseconds that every shape measured: `alone` with one tile to a CU, `full` with `resident` tiles
-// on every CU (512 products of 4096 x 7168 and smaller, bf16).  The shapes, at 32768 x 4096 x 7168 over 32 groups:
-// 256 x 256 1.77 ms, 128 x 256 2.03, 64 x 128 3.14, 32 x 128 5.5, 32 x 64 5.1; at 512 x 512 x 512 over 4 groups:
-// 14.3, 9.9, 7.4, 6.2, 5.4 us; at 1024 x 7168 x 2048 over 32 groups (weights streamed) 210, 201, 183, 191, 202 us.
+// on every CU.  The shapes in this order, bf16: at 32768 x 4096 x 7168 over 32 groups 1.77 ms, 2.03, 3.14, 5.5, 5.1;
+// at 512 x 512 x 512 over 4 groups 14.4, 9.8, 7.3, 6.1, 5.4, 6.1, 8.3 us; at 1024 x 7168 x 2048 over 32 groups
+// (weights streamed) 183, 175, 170, 188, 202, 240, 194 us; at 64 x 4096 x 7168, one group, 70, 52, 48, 35, 28, 19,
+// 53 us; at 1500 x 2048 x 4096 over 4 groups 80, 48, 46, 69, 82, 84, 38 us.
 struct RowShape {
     int bm, bn, resident;
     double fixed, alone, full;
 };
-constexpr RowShape kRowShapes[] = {{256, 256, 1, 8.5, 1.08, 1.70},
+enum { kShape256, kShape128, kShape64, kShape32, kShapeLeast, kShapeDeep, kShapeHalved };
+constexpr RowShape kRowShapes[] = {{256, 256, 1, 8.5, 1.08, 1.70},    // quadrants
                                    {128, 256, 1, 5.5, 0.58, 1.02},
                                    {64, 128, 2, 4.2, 0.40, 0.84},
                                    {32, 128, 2, 3.8, 0.29, 0.715},
-                                   {32, 64, 2, 3.6, 0.21, 0.35}};
+                                   {32, 64, 2, 3.6, 0.21, 0.35},      // the ones from here on are the forward's only
+                                   {32, 64, 1, 4.8, 0.125, 0.26},     // four groups of waves along the contraction
+                                   {128, 128, 1, 5.0, 0.50, 0.62}};   // two groups
 // choices: how many of them the product has.  Groups end inside a tile, half a tile to a group on average.
 inline int pick_row_shape(int rows, int cols, int depth, int groups, int choices) {
     int best = 0;

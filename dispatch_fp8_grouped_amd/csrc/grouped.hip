@@ -19,6 +19,7 @@ struct GroupedArgs {
     uint32_t* status;
     int rows, n, k, groups;
     int accumulate;
+    int parts;             // backward_weight: parts of a group's rows, each with its own output
 };
 
 // One tile of out = P Q^T with loop L; `out` points at the tile's first row and column, rows and cols exist there.
@@ -76,7 +77,8 @@ __global__ __launch_bounds__(L::kThreads) void grouped_weight_kernel(GroupedArgs
     const int ntm = (a.n + BM - 1) / BM, ntq = (a.k + BN - 1) / BN;
     // work-groups b with equal b % 8 share an XCD: each XCD takes an eighth of every group's tiles, since the
     // groups differ in length (whole groups per XCD left the XCDs of short groups idle half of the time)
-    const int per = (ntm * ntq + 7) >> 3, b = blockIdx.x >> 3, nth = b / per, li = (blockIdx.x & 7) * per + b - nth * per;
+    const int per = (ntm * ntq + 7) >> 3, part = (int)((blockIdx.x >> 3) % a.parts), b = (int)((blockIdx.x >> 3) / a.parts), nth = b / per,
+              li = (blockIdx.x & 7) * per + b - nth * per;
     if (nth >= a.groups || li >= ntm * ntq) return;
     const int g = a.groups <= 64 ? group_by_length(a.off, a.groups, a.rows, nth, lane) : nth;
     // bands of 8 row tiles, as the row products have bands of column tiles
@@ -88,11 +90,16 @@ __global__ __launch_bounds__(L::kThreads) void grouped_weight_kernel(GroupedArgs
     lo = __builtin_amdgcn_readfirstlane(lo);
     cnt = __builtin_amdgcn_readfirstlane(cnt);
     if (bad && li == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, MEGA_MOE_STATUS_BAD_LAYOUT);
-    if (cnt == 0 && a.accumulate) return;
+    if (cnt == 0 && a.accumulate && a.parts == 1) return;
+    if (a.parts > 1) {
+        const int share = ((cnt + kStepK - 1) / kStepK + a.parts - 1) / a.parts * kStepK, from = min(part * share, cnt);
+        lo += from;
+        cnt = min(cnt - from, share);
+    }
     typename L::Acc acc[L::QI][L::MI];
     const Operand P{a.p + (size_t)lo * a.n, m0, a.n, cnt}, Q{a.q + (size_t)lo * a.k, q0, a.k, cnt};
     L::run(P, Q, smem, wave, lane, acc);
-    const size_t at = ((size_t)g * a.n + m0) * a.k + q0;
+    const size_t at = (((size_t)part * a.groups + g) * a.n + m0) * a.k + q0;
     if constexpr (kFp32) {
         float* out = static_cast<float*>(a.out) + at;
         store_tile<L, 4>(
@@ -108,14 +115,34 @@ __global__ __launch_bounds__(L::kThreads) void grouped_weight_kernel(GroupedArgs
     }
 }
 
+// dw = the parts added up in their order (dw += with accumulate); values is a multiple of 8
+template <class T, bool kFp32>
+__global__ __launch_bounds__(256) void grouped_join_kernel(const float* parts, int n_parts, size_t values, void* out,
+                                                           int accumulate) {
+    for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4; i < values; i += (size_t)gridDim.x * 1024) {
+        f32x4 v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int s = 0; s < n_parts; ++s) v += *reinterpret_cast<const f32x4*>(parts + s * values + i);
+        if constexpr (kFp32) {
+            f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(out) + i);
+            *o = accumulate ? *o + v : v;
+        } else {
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
+        }
+    }
+}
+
 bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
+
+bool sizes_supported(int64_t rows, int32_t n, int32_t k, int32_t groups) {
+    return rows <= MEGA_MOE_MAX_GROUP_ROWS && n >= 8 && n <= MEGA_MOE_MAX_GROUP_COLS && n % 8 == 0 && k >= 8 &&
+           k <= MEGA_MOE_MAX_GROUP_COLS && k % 8 == 0 && groups >= 1 && groups <= MEGA_MOE_MAX_LOCAL_EXPERTS;
+}
 
 int32_t check_grouped(const void* p, const void* q, const int32_t* off, const void* out, int64_t rows, int32_t n,
                       int32_t k, int32_t groups, int32_t dtype, const uint32_t* status, bool weight) {
     if (rows < 0 || n < 0 || k < 0 || groups < 0) return MEGA_MOE_ERR_INVALID_ARG;
-    if (rows > MEGA_MOE_MAX_GROUP_ROWS || n < 8 || n > MEGA_MOE_MAX_GROUP_COLS || n % 8 || k < 8 ||
-        k > MEGA_MOE_MAX_GROUP_COLS || k % 8 || groups < 1 || groups > MEGA_MOE_MAX_LOCAL_EXPERTS ||
-        (dtype != MEGA_MOE_BF16 && dtype != MEGA_MOE_FP16))
+    if (!sizes_supported(rows, n, k, groups) || (dtype != MEGA_MOE_BF16 && dtype != MEGA_MOE_FP16))
         return MEGA_MOE_ERR_UNSUPPORTED;
     if (!off || ((uintptr_t)off & 3u) || ((uintptr_t)status & 3u)) return MEGA_MOE_ERR_INVALID_ARG;
     const bool any = rows > 0;
@@ -134,40 +161,73 @@ hipError_t launch_rows_with(const GroupedArgs& a, hipStream_t st) {
 
 template <class T, bool B>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t st) {
-    // a KS operand needs 128 columns: the narrowest shape is the forward's only
     using Wide = TileLoop<T, false, B, 128, 256, 2, 4, 3>;
     using Low = TileLoop<T, false, B, 64, 256, 1, 8, 3>;
     using Mid = TileLoop<T, false, B, 64, 128, 1, 4, 3>;
     using Small = TileLoop<T, false, B, 32, 128, 1, 4, 4>;
-    switch (pick_row_shape(a.rows, B ? a.k : a.n, B ? a.n : a.k, a.groups, B ? 4 : 5)) {
-        case 0: return launch_rows_with<QuadLoop<T, false, B, 256, 256, 4, 2>, Wide, T, B, 256, 256>(a, st);
-        case 1: return launch_rows_with<Wide, Low, T, B, 128, 256>(a, st);
-        case 2: return launch_rows_with<Mid, Mid, T, B, 64, 128>(a, st);
-        case 3: return launch_rows_with<Small, Small, T, B, 32, 128>(a, st);
-        default:
-            if constexpr (!B) {
-                using Least = TileLoop<T, false, false, 32, 64, 1, 4, 5>;
-                return launch_rows_with<Least, Least, T, false, 32, 64>(a, st);
-            }
-            return hipErrorInvalidValue;
+    // a KS operand needs 128 columns, and gained nothing from groups of waves (300 x 6000 x 600: 31.6 us with and
+    // without): those shapes are the forward's only
+    const int shape = pick_row_shape(a.rows, B ? a.k : a.n, B ? a.n : a.k, a.groups, B ? kShape32 + 1 : kShapeHalved + 1);
+    if (shape == kShape256)
+        return launch_rows_with<QuadLoop<T, false, B, 256, 256, 4, 2>, Wide, T, B, 256, 256>(a, st);
+    if (shape == kShape128) return launch_rows_with<Wide, Low, T, B, 128, 256>(a, st);
+    if (shape == kShape64) return launch_rows_with<Mid, Mid, T, B, 64, 128>(a, st);
+    if (shape == kShape32) return launch_rows_with<Small, Small, T, B, 32, 128>(a, st);
+    if constexpr (!B) {
+        using Least = TileLoop<T, false, false, 32, 64, 1, 4, 5>;
+        using Deep = TileLoop<T, false, false, 32, 64, 1, 4, 3, 4>;
+        using Halved = TileLoop<T, false, false, 128, 128, 2, 2, 2, 2>;
+        if (shape == kShapeLeast) return launch_rows_with<Least, Least, T, false, 32, 64>(a, st);
+        if (shape == kShapeDeep) return launch_rows_with<Deep, Deep, T, false, 32, 64>(a, st);
+        return launch_rows_with<Halved, Halved, T, false, 128, 128>(a, st);
     }
+    return hipErrorInvalidValue;
 }
 
 template <class L, class T, bool kFp32, int BM, int BN>
 hipError_t launch_weight_with(const GroupedArgs& a, hipStream_t st) {
     const int64_t tiles = (int64_t)((a.n + BM - 1) / BM) * ((a.k + BN - 1) / BN);
-    hipLaunchKernelGGL((grouped_weight_kernel<L, T, kFp32, BM, BN>), dim3((uint32_t)((tiles + 7) / 8 * 8 * a.groups)),
-                       dim3(L::kThreads), 0, st, a);
+    hipLaunchKernelGGL((grouped_weight_kernel<L, T, kFp32, BM, BN>),
+                       dim3((uint32_t)((tiles + 7) / 8 * 8 * a.groups * a.parts)), dim3(L::kThreads), 0, st, a);
     return hipGetLastError();
 }
 
+// 256 x 256 tiles where they fill the CUs (16384 rows, 32 x 4096 x 7168, fp32: 1.44 ms against 1.75 with
+// 128 x 128).  Below that the smaller ones, four times as many, and where these leave CUs without work and the
+// groups are long, the rows are split into parts of at least four steps (of an average group) that a second launch adds up.
+constexpr int kWeightLarge = 192;
+int64_t weight_tiles(int n, int k, int groups, int edge) {
+    return (int64_t)groups * ((n + edge - 1) / edge) * ((k + edge - 1) / edge);
+}
+int weight_parts(int64_t rows, int n, int k, int groups) {
+    if (weight_tiles(n, k, groups, 256) >= kWeightLarge) return 1;
+    const int64_t by_tiles = 256 / weight_tiles(n, k, groups, 128), by_rows = rows / groups / (4 * kStepK);
+    const int64_t parts = by_tiles < by_rows ? by_tiles : by_rows;
+    return (int)(parts < 1 ? 1 : parts);
+}
+
 template <class T, bool kFp32>
-hipError_t launch_weight(const GroupedArgs& a, hipStream_t st) {
-    // 256 x 256 tiles where they fill the CUs (16384 rows, 32 x 4096 x 7168, fp32: 1.44 ms against 1.75 with
-    // 128 x 128); below that the smaller ones, four times as many
-    const int64_t large = (int64_t)a.groups * ((a.n + 255) / 256) * ((a.k + 255) / 256);
-    if (large >= 192) return launch_weight_with<QuadLoop<T, true, true, 256, 256, 2, 4>, T, kFp32, 256, 256>(a, st);
-    return launch_weight_with<TileLoop<T, true, true, 128, 128, 2, 2, 2>, T, kFp32, 128, 128>(a, st);
+hipError_t launch_weight(GroupedArgs a, void* workspace, hipStream_t st) {
+    if (weight_tiles(a.n, a.k, a.groups, 256) >= kWeightLarge)
+        return launch_weight_with<QuadLoop<T, true, true, 256, 256, 2, 4>, T, kFp32, 256, 256>(a, st);
+    using L = TileLoop<T, true, true, 128, 128, 2, 2, 2>;
+    if (a.parts == 1) return launch_weight_with<L, T, kFp32, 128, 128>(a, st);
+    void* dw = a.out;
+    const int accumulate = a.accumulate;
+    a.out = workspace;
+    a.accumulate = 0;
+    const hipError_t e = launch_weight_with<L, T, true, 128, 128>(a, st);
+    if (e != hipSuccess) return e;
+    const size_t values = (size_t)a.groups * a.n * a.k;
+    const size_t blocks = (values + 1023) / 1024;
+    hipLaunchKernelGGL((grouped_join_kernel<T, kFp32>), dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st,
+                       static_cast<const float*>(workspace), a.parts, values, dw, accumulate);
+    return hipGetLastError();
+}
+
+// a launch has fewer than 2^32 threads: at most 2^22 tiles of any shape
+bool too_many_tiles(int64_t rows, int cols, int groups) {
+    return (rows / 128 + groups) * ((cols + 127) / 128) > (int64_t)1 << 22;
 }
 
 }  // namespace
@@ -180,9 +240,11 @@ extern "C" {
 int32_t mega_moe_grouped_forward(const void* x, const void* w, const int32_t* offsets, void* y, int64_t rows, int32_t n,
                                  int32_t k, int32_t groups, int32_t dtype, uint32_t* device_status, void* stream) {
     const int32_t rc = check_grouped(x, w, offsets, y, rows, n, k, groups, dtype, device_status, false);
-    if (rc || rows == 0) return rc;
+    if (rc) return rc;
+    if (too_many_tiles(rows, n, groups)) return MEGA_MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MEGA_MOE_OK;
     const GroupedArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(w), y, offsets, device_status,
-                        (int)rows, n, k, groups, 0};
+                        (int)rows, n, k, groups, 0, 1};
     hipStream_t st = static_cast<hipStream_t>(stream);
     const hipError_t e = dtype == MEGA_MOE_BF16 ? launch_rows<Bf16, false>(a, st) : launch_rows<Fp16, false>(a, st);
     return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
@@ -192,31 +254,47 @@ int32_t mega_moe_grouped_backward_rows(const void* dy, const void* w, const int3
                                        int32_t n, int32_t k, int32_t groups, int32_t dtype, uint32_t* device_status,
                                        void* stream) {
     const int32_t rc = check_grouped(dy, w, offsets, dx, rows, n, k, groups, dtype, device_status, false);
-    if (rc || rows == 0) return rc;
+    if (rc) return rc;
+    if (too_many_tiles(rows, k, groups)) return MEGA_MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MEGA_MOE_OK;
     const GroupedArgs a{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(w), dx, offsets, device_status,
-                        (int)rows, n, k, groups, 0};
+                        (int)rows, n, k, groups, 0, 1};
     hipStream_t st = static_cast<hipStream_t>(stream);
     const hipError_t e = dtype == MEGA_MOE_BF16 ? launch_rows<Bf16, true>(a, st) : launch_rows<Fp16, true>(a, st);
     return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
+int32_t mega_moe_grouped_weight_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t groups, uint64_t* bytes_out) {
+    if (!bytes_out || rows < 0 || n < 0 || k < 0 || groups < 0) return MEGA_MOE_ERR_INVALID_ARG;
+    if (!sizes_supported(rows, n, k, groups)) return MEGA_MOE_ERR_UNSUPPORTED;
+    const int parts = weight_parts(rows, n, k, groups);
+    *bytes_out = parts > 1 ? (uint64_t)parts * groups * n * k * 4 : 0;
+    return MEGA_MOE_OK;
+}
+
 int32_t mega_moe_grouped_backward_weight(const void* dy, const void* x, const int32_t* offsets, void* dw, int64_t rows,
                                          int32_t n, int32_t k, int32_t groups, int32_t dtype, int32_t out_dtype,
-                                         int32_t accumulate, uint32_t* device_status, void* stream) {
+                                         int32_t accumulate, void* workspace, uint64_t workspace_bytes,
+                                         uint32_t* device_status, void* stream) {
     const int32_t rc = check_grouped(dy, x, offsets, dw, rows, n, k, groups, dtype, device_status, true);
     if (rc) return rc;
     if (out_dtype != dtype && out_dtype != MEGA_MOE_FP32) return MEGA_MOE_ERR_UNSUPPORTED;
     if (accumulate && out_dtype != MEGA_MOE_FP32) return MEGA_MOE_ERR_UNSUPPORTED;
-    // 32-bit tile numbers, and a launch of fewer than 2^32 threads
-    if ((int64_t)groups * ((n + 127) / 128) * ((k + 127) / 128) > (int64_t)1 << 22) return MEGA_MOE_ERR_UNSUPPORTED;
+    // a launch has fewer than 2^32 threads
+    if (weight_tiles(n, k, groups, 256) > (int64_t)1 << 21) return MEGA_MOE_ERR_UNSUPPORTED;
+    const int parts = weight_parts(rows, n, k, groups);
+    if (parts > 1) {
+        if (!aligned16(workspace)) return MEGA_MOE_ERR_INVALID_ARG;
+        if (workspace_bytes < (uint64_t)parts * groups * n * k * 4) return MEGA_MOE_ERR_WORKSPACE_TOO_SMALL;
+    }
     const GroupedArgs a{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x), dw, offsets, device_status,
-                        (int)rows, n, k, groups, accumulate != 0};
+                        (int)rows, n, k, groups, accumulate != 0, parts};
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e;
     if (out_dtype == MEGA_MOE_FP32)
-        e = dtype == MEGA_MOE_BF16 ? launch_weight<Bf16, true>(a, st) : launch_weight<Fp16, true>(a, st);
+        e = dtype == MEGA_MOE_BF16 ? launch_weight<Bf16, true>(a, workspace, st) : launch_weight<Fp16, true>(a, workspace, st);
     else
-        e = dtype == MEGA_MOE_BF16 ? launch_weight<Bf16, false>(a, st) : launch_weight<Fp16, false>(a, st);
+        e = dtype == MEGA_MOE_BF16 ? launch_weight<Bf16, false>(a, workspace, st) : launch_weight<Fp16, false>(a, workspace, st);
     return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 

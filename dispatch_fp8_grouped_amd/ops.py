@@ -30,6 +30,7 @@ _SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 
 # Exported symbols of include/mega_moe_ops.h
 OPS_EXPORTS = ("mega_moe_grouped_forward", "mega_moe_grouped_backward_rows", "mega_moe_grouped_backward_weight",
+               "mega_moe_grouped_weight_workspace_bytes",
                "mega_moe_router_topk", "mega_moe_router_backward", "mega_moe_group_workspace_bytes",
                "mega_moe_group_by_expert", "mega_moe_adapter_workspace_bytes", "mega_moe_adapter_forward")
 
@@ -52,7 +53,8 @@ def _bind(L):
     rows = [vp, vp, vp, vp, i64, i32, i32, i32, i32]
     L.mega_moe_grouped_forward.argtypes = rows + [vp, vp]
     L.mega_moe_grouped_backward_rows.argtypes = rows + [vp, vp]
-    L.mega_moe_grouped_backward_weight.argtypes = rows + [i32, i32, vp, vp]
+    L.mega_moe_grouped_backward_weight.argtypes = rows + [i32, i32, vp, u64, vp, vp]
+    L.mega_moe_grouped_weight_workspace_bytes.argtypes = [i64, i32, i32, i32, ctypes.POINTER(u64)]
     cfg = ctypes.POINTER(mega_moe_router_config)
     L.mega_moe_router_topk.argtypes = [cfg, vp, vp, vp, vp, vp]
     L.mega_moe_router_backward.argtypes = [cfg, vp, vp, vp, vp, vp]
@@ -77,10 +79,21 @@ def mega_moe_grouped_backward_rows(dy, w, offsets, dx, rows, n, k, groups, dtype
               "mega_moe_grouped_backward_rows")
 
 
+def mega_moe_grouped_weight_workspace_bytes(rows: int, n: int, k: int, groups: int) -> int:
+    out = ctypes.c_uint64(0)
+    _mm._check(_mm.lib().mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups, ctypes.byref(out)),
+               "mega_moe_grouped_weight_workspace_bytes")
+    return out.value
+
+
 def mega_moe_grouped_backward_weight(dy, x, offsets, dw, rows, n, k, groups, dtype, out_dtype, accumulate=False,
-                                     device_status=None, stream=None):
+                                     workspace=None, workspace_bytes=None, device_status=None, stream=None):
+    nbytes = workspace_bytes
+    if nbytes is None:
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _mm._check(_mm.lib().mega_moe_grouped_backward_weight(_mm._ptr(dy), _mm._ptr(x), _mm._ptr(offsets), _mm._ptr(dw), rows, n,
                                                         k, groups, dtype, out_dtype, 1 if accumulate else 0,
+                                                        _mm._ptr(workspace), nbytes,
                                                         _mm._ptr(device_status), _mm._stream(stream)),
               "mega_moe_grouped_backward_weight")
 
@@ -236,13 +249,16 @@ def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=Fal
         raise ValueError("accumulate needs a float32 `out`")
     if status is not None:
         _want("status", status, (1,), (torch.int32,), x.device)
+    nbytes = mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups)
     with _Call(x.device, stream) as raw:
         if out is None:
             out = torch.empty((groups, n, k), dtype=dtype, device=x.device)
         else:
             _want("out", out, (groups, n, k), (dtype,), x.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
         mega_moe_grouped_backward_weight(dy, x, offsets, out, rows, n, k, groups, kinds[x.dtype],
-                                         FP32 if dtype == torch.float32 else kinds[dtype], accumulate, status, raw)
+                                         FP32 if dtype == torch.float32 else kinds[dtype], accumulate, workspace, nbytes,
+                                         status, raw)
     return out
 
 

@@ -52,10 +52,12 @@ extern "C" {
  *   dtype      MEGA_MOE_BF16 or MEGA_MOE_FP16, of every operand
  *   out_dtype  (backward_weight) dtype or MEGA_MOE_FP32
  *   accumulate (backward_weight) nonzero: dw += instead of dw =, with out_dtype MEGA_MOE_FP32 only
+ *   workspace  (backward_weight) mega_moe_grouped_weight_workspace_bytes() bytes, 0 for most sizes (NULL then): few
+ *              and small weights with many rows split the sum; its contents do not matter
  * backward_weight writes zeros for a group without rows (leaves it as it was when accumulating).
  * With rows == 0, forward and backward_rows do nothing and the row pointers may be NULL.
  * Errors: INVALID_ARG (null or misaligned pointer, negative size), UNSUPPORTED (size or type outside the
- * limits), HIP. */
+ * limits, or an output of more than 2^22 tiles of 128 x 128), WORKSPACE_TOO_SMALL, HIP. */
 int32_t mega_moe_grouped_forward(const void* x, const void* w, const int32_t* offsets, void* y, int64_t rows,
                                  int32_t n, int32_t k, int32_t groups, int32_t dtype, uint32_t* device_status,
                                  void* stream);
@@ -64,8 +66,10 @@ int32_t mega_moe_grouped_backward_rows(const void* dy, const void* w, const int3
                                        uint32_t* device_status, void* stream);
 int32_t mega_moe_grouped_backward_weight(const void* dy, const void* x, const int32_t* offsets, void* dw,
                                          int64_t rows, int32_t n, int32_t k, int32_t groups, int32_t dtype,
-                                         int32_t out_dtype, int32_t accumulate, uint32_t* device_status,
-                                         void* stream);
+                                         int32_t out_dtype, int32_t accumulate, void* workspace,
+                                         uint64_t workspace_bytes, uint32_t* device_status, void* stream);
+int32_t mega_moe_grouped_weight_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t groups,
+                                                uint64_t* bytes_out /* host */);
 
 /* ------------------------------------------------------------------ router */
 #define MEGA_MOE_SCORE_SOFTMAX 0   /* s = softmax of the token's logits over all its unmasked experts */

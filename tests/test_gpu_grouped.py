@@ -85,6 +85,12 @@ SHAPES = [
     ([1, 300, 8000], 520, 3080),
     ([9000], 264, 4104),
     ([3000, 17, 0, 900], 4104, 2056),
+    # the shapes with groups of waves along the contraction; weights whose rows are split into parts
+    ([64], 2056, 7168),
+    ([3], 520, 8200),
+    ([700, 0, 520, 300], 2056, 4104),
+    ([20000], 72, 64),
+    ([9000, 0, 3, 4000], 136, 264),
 ]
 
 
@@ -140,8 +146,9 @@ def test_nan_stays_in_its_row_and_its_group():
     assert torch.isnan(dw[1]).all()
 
 
-def test_accumulate_into_fp32_gradient():
-    x, dy, w, off_t, off = make([30, 0, 200], 136, 264, torch.bfloat16, seed=7)
+@pytest.mark.parametrize("counts", [[30, 0, 200], [3000, 0, 2500]])
+def test_accumulate_into_fp32_gradient(counts):
+    x, dy, w, off_t, off = make(counts, 136, 264, torch.bfloat16, seed=7)
     before = torch.randn(3, 136, 264, device="cuda")
     dw = before.clone()
     assert mm.grouped_backward_weight(dy, x, off_t, out=dw, accumulate=True) is dw

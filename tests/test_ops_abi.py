@@ -27,8 +27,10 @@ def test_library_exports_every_declared_operator():
         assert callable(getattr(mm, n))
 
 
-def grouped(fn, p=P, q=P, off=P, out=P, rows=4, n=16, k=16, groups=2, dtype=mm.BF16, status=None, more=()):
-    return getattr(mm.lib(), fn)(p, q, off, out, rows, n, k, groups, dtype, *more, status, None)
+def grouped(fn, p=P, q=P, off=P, out=P, rows=4, n=16, k=16, groups=2, dtype=mm.BF16, status=None, more=(), ws=()):
+    if more and not ws:
+        ws = (P, 1 << 40)
+    return getattr(mm.lib(), fn)(p, q, off, out, rows, n, k, groups, dtype, *more, *ws, status, None)
 
 
 @pytest.mark.parametrize("fn,more", [("mega_moe_grouped_forward", ()), ("mega_moe_grouped_backward_rows", ()),
@@ -45,7 +47,18 @@ def test_grouped_refusals(fn, more):
         assert grouped(fn, more=(mm.FP16, 0)) == mm.ERR_UNSUPPORTED          # bf16 operands, fp16 output
         assert grouped(fn, more=(mm.BF16, 1)) == mm.ERR_UNSUPPORTED          # accumulating in 16 bits
         assert grouped(fn, more=more, n=65536, k=65536, groups=1024) == mm.ERR_UNSUPPORTED   # too many tiles
+        need = mm.mega_moe_grouped_weight_workspace_bytes(9000, 16, 16, 2)
+        assert need > 0 and mm.mega_moe_grouped_weight_workspace_bytes(9000, 4096, 7168, 32) == 0
+        assert grouped(fn, more=more, rows=9000, ws=(P, need - 1)) == mm.ERR_WORKSPACE_TOO_SMALL
+        assert grouped(fn, more=more, rows=9000, ws=(None, need)) == mm.ERR_INVALID_ARG
+        assert grouped(fn, more=more, rows=9000, ws=(ODD, need)) == mm.ERR_INVALID_ARG
+        out = ctypes.c_uint64(0)
+        lib = mm.lib()
+        assert lib.mega_moe_grouped_weight_workspace_bytes(4, 16, 16, 2, None) == mm.ERR_INVALID_ARG
+        assert lib.mega_moe_grouped_weight_workspace_bytes(-4, 16, 16, 2, ctypes.byref(out)) == mm.ERR_INVALID_ARG
+        assert lib.mega_moe_grouped_weight_workspace_bytes(4, 12, 16, 2, ctypes.byref(out)) == mm.ERR_UNSUPPORTED
     else:
+        assert grouped(fn, rows=1 << 26, n=65536, k=65536) == mm.ERR_UNSUPPORTED       # too many tiles
         assert grouped(fn, p=None, out=None, rows=0) == mm.OK                # nothing to do
 
 
