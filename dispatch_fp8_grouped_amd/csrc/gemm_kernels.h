@@ -310,6 +310,177 @@ __device__ __forceinline__ void store_halves(const typename L::Acc (&acc)[L::QI]
         [&](int m, int c, i32x4 v) { *reinterpret_cast<i32x4*>(out + (size_t)m * ld + c) = v; });
 }
 
+// A stream of tiles with two KS operands, for products whose contraction is short beside their output: QuadLoop's
+// steps one tile after the other, the next tile's first two steps loading under the last two of the current one, and
+// the output leaving while the next tile is multiplied.  (A tile per work-group spent as long on its first loads and
+// its stores as on eight steps' MFMAs.)
+//
+// The waits count instructions, and stores count like loads, in order: after a tile's kStores stores the three waits
+// for groups that were issued before them allow that many more to be outstanding.  So the number of stores of a tile
+// is a constant: the stores of rows or columns that do not exist go past their descriptor's end.
+//
+// Tiles: next(first row, first column, contraction length) sets the next tile's operands and output, false at the end.
+template <class T, int kBytes>
+struct KsStream {
+    static constexpr int BM = 256, BN = 256;
+    using L = QuadLoop<T, true, true, BM, BN, 4, 2>;
+    static constexpr int kThreads = L::kThreads, MI = L::MI, QI = L::QI, MH = L::MH, QH = L::QH, kInstr = L::kInstr;
+    // 16 rows of 128 bytes, and their padding, per wave beside the stages
+    static constexpr int kRun = 8 / kBytes, kStride = 128 + 16, kSlot = 16 * kStride;
+    static constexpr int kLds = L::kLds + L::kWaves * kSlot;
+    static constexpr int kStores = MI * (QI / kRun) * 2;
+    static_assert(2 * kInstr + kStores < 64, "vmcnt");
+    using Lanes = KsLanes<BM / 2, L::kWaves>;
+
+    // All wave-uniform (readfirstlane in of()).
+    struct Tile {
+        const uint16_t *p, *q;     // contraction row 0, column 0 of the operands
+        int p_col, q_col;          // the tile's first columns
+        int len, steps;            // contraction; at least two steps, so that a step's loads belong to its tile or the next
+        char* out;                 // first row and column of the tile
+        int rows, cols;            // that exist from there on
+    };
+    template <class U>
+    static __device__ __forceinline__ U* uniform(U* ptr) {
+        const uint64_t v = (uint64_t)(uintptr_t)ptr;
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+        return (U*)(uintptr_t)((uint64_t)hi << 32 | lo);
+    }
+    static __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+    // exists: false for the end of the stream (no steps, and nothing is read)
+    static __device__ __forceinline__ Tile of(bool exists, const uint16_t* p, int p_col, const uint16_t* q, int q_col, int len, char* out,
+                                              int rows, int cols) {
+        const int n = exists ? uniform(len) : 0;
+        return Tile{uniform(p),   uniform(q),    uniform(p_col), uniform(q_col), n, exists ? max((n + kStepK - 1) / kStepK, 2) : 0,
+                    uniform(out), uniform(rows), uniform(cols)};
+    }
+    static __device__ __forceinline__ Tile either(bool first, const Tile& a, const Tile& b) {
+        return Tile{first ? a.p : b.p,         first ? a.q : b.q,       first ? a.p_col : b.p_col,
+                    first ? a.q_col : b.q_col, first ? a.len : b.len,   first ? a.steps : b.steps,
+                    first ? a.out : b.out,     first ? a.rows : b.rows, first ? a.cols : b.cols};
+    }
+
+    // Accumulators to `out` through the wave's slot, kStores store instructions; each lane's 16 bytes go through
+    // change(address, bytes) where they exist.
+    template <class C>
+    static __device__ __forceinline__ void store(const Tile& t, int ld, const f32x4 (&acc)[QI][MI], uint8_t* slot, int wave,
+                                                 C change) {
+        const uint32_t ldb = (uint32_t)ld * kBytes;
+        // addresses are computed here and not before the steps, whose registers are full
+        int lane = __lane_id();
+        asm volatile("" : "+v"(lane));
+        const auto desc = __builtin_amdgcn_make_buffer_rsrc(t.out, 0, (int)((uint32_t)min(t.rows, BM) * ldb), 0x00020000);
+#pragma unroll
+        for (int j = 0; j < MI; ++j)
+#pragma unroll
+            for (int run = 0; run < QI / kRun; ++run) {
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    const f32x4 v = acc[run * kRun + i][j];
+                    uint8_t* at = slot + (lane & 15) * kStride + (i * 16 + (lane >> 4) * 4) * kBytes;
+                    if constexpr (kBytes == 4) *reinterpret_cast<f32x4*>(at) = v;
+                    else *reinterpret_cast<u32x2*>(at) = u32x2{T::pack(v[0], v[1]), T::pack(v[2], v[3])};
+                }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = h * 8 + (lane >> 3), m = L::row(wave, j) + r;
+                    const int c = L::col(wave, run * kRun) + (lane & 7) * (16 / kBytes);
+                    i32x4 v = *reinterpret_cast<const i32x4*>(slot + r * kStride + (lane & 7) * 16);
+                    const bool exists = m < t.rows && c < t.cols;
+                    const uint32_t off = exists ? (uint32_t)m * ldb + (uint32_t)c * kBytes : kPastEnd;
+                    v = change(t.out + off, exists, v);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), desc, (int)off, 0, 0);
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+    }
+
+    template <class N, class C>
+    static __device__ __forceinline__ void run(N next, int ld_p, int ld_q, int ld_out, uint8_t* smem, int wave, int lane,
+                                               C change) {
+        const int wm = wave / 2, wn = wave % 2;
+        const uint32_t lds = lds_byte(smem);
+        uint8_t* slot = smem + L::kLds + wave * kSlot;
+        const Lanes lp(ld_p, wave, lane), lq(ld_q, wave, lane);
+        Tile cur = next();
+        if (cur.steps == 0) return;
+        Tile ahead = next();
+        f32x4 acc[QI][MI];
+        i32x4 p0[2][MH], p1[2][MH], q0[2][QH], q1[2][QH];
+        const auto p_step = [&](const Tile& t, int h, int s) { return KsWhere(t.p, t.p_col + h * (BM / 2), ld_p, t.len).step(s); };
+        const auto q_step = [&](const Tile& t, int h, int s) { return KsWhere(t.q, t.q_col + h * (BN / 2), ld_q, t.len).step(s); };
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 ps = p_step(cur, h, s), qs = q_step(cur, h, s);
+#pragma unroll
+                for (int d = 0; d < L::kPInstr; ++d) lp.load(ps, d, lds + L::p_at(s, h), wave);
+#pragma unroll
+                for (int d = 0; d < L::kQInstr; ++d) lq.load(qs, d, lds + L::q_at(s, h), wave);
+            }
+        wait_vm_barrier<3 * kInstr>();
+#pragma unroll
+        for (int r = 0; r < 2 * MH; ++r) L::read_p(r, smem + L::p_at(0, 0), wm, lane, p0);
+#pragma unroll
+        for (int r = 0; r < 2 * QH; ++r) L::read_q(r, smem + L::q_at(0, 0), wn, lane, q0);
+        int b = 0, waits = 0;            // waits: how many more may leave a tile's stores outstanding
+        const auto wait = [&] {
+            if (waits > 0) {
+                wait_vm_barrier<2 * kInstr + kStores>();
+                --waits;
+            } else {
+                wait_vm_barrier<2 * kInstr>();
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        while (true) {
+#pragma unroll
+            for (int i = 0; i < QI; ++i)
+#pragma unroll
+                for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < cur.steps; ++s) {
+                const int pb = b * 2 * L::kPHalf, qb = b * 2 * L::kQHalf, pn = 2 * L::kPHalf - pb, qn = 2 * L::kQHalf - qb;
+                const bool here = s + 2 < cur.steps;
+                const int s2 = here ? s + 2 : s + 2 - cur.steps;
+                const Tile t = either(here, cur, ahead);
+                wait();
+                {
+                    const u32x4 ps = p_step(t, 0, s2), qs = q_step(t, 0, s2);
+                    L::template multiply<0, 2 * QH, 2 * MH, 4 * QH, 2>(
+                        p0, q0, q1, acc, [&](int r) { L::read_q(r, smem + L::q_at(0, 1) + qb, wn, lane, q1); },
+                        [&](int r) { L::read_p(r, smem + L::p_at(0, 1) + pb, wm, lane, p1); },
+                        [&](int d) {
+                            if (d < L::kPInstr) lp.load(ps, d, lds + L::p_at(0, 0) + pb, wave);
+                            else lq.load(qs, d - L::kPInstr, lds + L::q_at(0, 0) + qb, wave);
+                        });
+                }
+                wait();
+                {
+                    int l = lane;                // read addresses again, for want of registers to keep them
+                    asm volatile("" : "+v"(l));
+                    const u32x4 ps = p_step(t, 1, s2), qs = q_step(t, 1, s2);
+                    L::template multiply<1, 2 * MH, 2 * QH, L::kQuad, 1>(
+                        p1, q0, q1, acc, [&](int r) { L::read_p(r, smem + L::p_at(0, 0) + pn, wm, l, p0); },
+                        [&](int r) { L::read_q(r, smem + L::q_at(0, 0) + qn, wn, l, q0); },
+                        [&](int d) {
+                            if (d < L::kPInstr) lp.load(ps, d, lds + L::p_at(0, 1) + pb, wave);
+                            else lq.load(qs, d - L::kPInstr, lds + L::q_at(0, 1) + qb, wave);
+                        });
+                }
+                b ^= 1;
+            }
+            store(cur, ld_out, acc, slot, wave, change);
+            waits = 3;
+            if (ahead.steps == 0) break;
+            cur = ahead;
+            ahead = next();
+        }
+        wait_vm_barrier<0>();
+    }
+};
+
 // Which tile shape a row product of these sizes runs with (forward and backward of the groups, the adapters'
 // shared product).  The time is estimated as `fixed` + steps * (a tile's time per step) * (rounds of tiles over the
 // CUs), with the microseconds that every shape measured: `alone` with one tile to a CU, `full` with `resident` tiles

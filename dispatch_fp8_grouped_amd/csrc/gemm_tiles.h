@@ -79,7 +79,7 @@ __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {
 // the stages apart, would drain every DMA in flight before each LDS read.
 __device__ __forceinline__ void dma_rows(u32x4 desc, uint32_t off, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :: "v"(off), "s"(desc), "s"(dst) : "memory", "m0");
+                 :: "v"(off), "s"(desc), "s"(__builtin_amdgcn_readfirstlane(dst)) : "memory", "m0");
 }
 // At most N of this wave's vector-memory operations still outstanding and its LDS reads returned; then barrier.
 template <int N>
@@ -140,36 +140,48 @@ struct KcTile {
     }
 };
 
-// The DMA of one KS operand tile of 64 contraction rows x W columns.
+// The DMA of one KS operand tile of 64 contraction rows x W columns: what depends on the lane, and what depends on
+// the tile.
 template <int W, int WAVES>
-struct KsTile {
+struct KsLanes {
     static constexpr int kRowsPerInstr = 512 / W, kInstr = kStepK / kRowsPerInstr / WAVES, kBytes = W * 128;
     static_assert(W >= 128, "eight 32-byte pairs to swizzle");
     static_assert(kInstr >= 1 && (kInstr == 1 || (kRowsPerInstr * WAVES) % 16 == 0), "the swizzle must not change with j");
-    const char* base;     // contraction row 0, first column of the tile
     uint32_t off[kInstr];
+    __device__ __forceinline__ KsLanes(int ld, int wave, int lane) {
+        const int r0 = wave * kRowsPerInstr + lane / (W / 8), pos = lane % (W / 8);
+        const int chunk = (((pos >> 1) ^ ks_swz(r0)) << 1) | (pos & 1);
+#pragma unroll
+        for (int j = 0; j < kInstr; ++j) off[j] = (uint32_t)(r0 + j * WAVES * kRowsPerInstr) * (uint32_t)(ld * 2) + chunk * 16;
+    }
+    __device__ __forceinline__ void load(u32x4 desc, int j, uint32_t lds, int wave) const {
+        dma_rows(desc, off[j], lds + (wave + j * WAVES) * 1024);
+    }
+};
+struct KsWhere {
+    const char* base;     // contraction row 0, first column of the tile
     uint32_t ldb, skip;   // bytes of a memory row; bytes before the tile's first column
-    int len;              // contraction rows
-    __device__ __forceinline__ KsTile(const void* p, int col0, int ld, int length, int wave, int lane) {
+    int len;              // contraction rows, 0 for a tile behind the last column
+    __device__ __forceinline__ KsWhere(const void* p, int col0, int ld, int length) {
         ldb = (uint32_t)ld * 2u;
         skip = (uint32_t)col0 * 2u;
         base = static_cast<const char*>(p) + skip;
         len = col0 < ld ? length : 0;
-        const int r0 = wave * kRowsPerInstr + lane / (W / 8), pos = lane % (W / 8);
-        const int chunk = (((pos >> 1) ^ ks_swz(r0)) << 1) | (pos & 1);
-#pragma unroll
-        for (int j = 0; j < kInstr; ++j) off[j] = (uint32_t)(r0 + j * WAVES * kRowsPerInstr) * ldb + chunk * 16;
     }
-    struct Step {
-        u32x4 desc;
-    };
-    __device__ __forceinline__ Step step(int s) const {
+    __device__ __forceinline__ u32x4 step(int s) const {
         const int k0 = s * kStepK, left = min(len - k0, kStepK);
-        return Step{buffer_of(base + (left > 0 ? (size_t)k0 * ldb : 0), left > 0 ? (uint32_t)left * ldb - skip : 0u)};
+        return buffer_of(base + (left > 0 ? (size_t)k0 * ldb : 0), left > 0 ? (uint32_t)left * ldb - skip : 0u);
     }
-    __device__ __forceinline__ void load(const Step& t, int j, uint32_t lds, int wave) const {
-        dma_rows(t.desc, off[j], lds + (wave + j * WAVES) * 1024);
-    }
+};
+template <int W, int WAVES>
+struct KsTile {
+    using Step = u32x4;
+    KsLanes<W, WAVES> lanes;
+    KsWhere where;
+    __device__ __forceinline__ KsTile(const void* p, int col0, int ld, int length, int wave, int lane)
+        : lanes(ld, wave, lane), where(p, col0, ld, length) {}
+    __device__ __forceinline__ Step step(int s) const { return where.step(s); }
+    __device__ __forceinline__ void load(const Step& t, int j, uint32_t lds, int wave) const { lanes.load(t, j, lds, wave); }
 };
 
 // One operand of a product tile.  KC: `p` points at the tile's first row, `extent` rows exist from there on.  KS:

@@ -115,6 +115,64 @@ __global__ __launch_bounds__(L::kThreads) void grouped_weight_kernel(GroupedArgs
     }
 }
 
+// backward_weight with enough large tiles for every CU: a stream of them per work-group, 32 work-groups to an XCD.
+// Each XCD takes an eighth of every group's tiles, longest group first, and its work-groups take turns.
+constexpr int kStreams = 32;
+template <class T, bool kFp32>
+__global__ __launch_bounds__(512) void grouped_weight_stream_kernel(GroupedArgs a) {
+    constexpr int kBytes = kFp32 ? 4 : 2;
+    using S = KsStream<T, kBytes>;
+    static_assert(S::kThreads == 512, "one launch");
+    __shared__ __align__(1024) uint8_t smem[S::kLds];
+    // the groups in the order of their tiles: longest first where 64 lanes can rank them (long and short ones in turn,
+    // so that stores meet MFMAs, took longer: 1.49 ms against 1.43 with skewed groups)
+    __shared__ int order_g[MEGA_MOE_MAX_LOCAL_EXPERTS], order_first[MEGA_MOE_MAX_LOCAL_EXPERTS],
+        order_rows[MEGA_MOE_MAX_LOCAL_EXPERTS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ntm = (a.n + S::BM - 1) / S::BM, ntq = (a.k + S::BN - 1) / S::BN, per = (ntm * ntq + 7) >> 3;
+    bool bad = false;
+    for (int e = threadIdx.x; e < a.groups; e += S::kThreads) {
+        int lo, cnt, place = e;
+        group_rows(a.off, e, a.rows, lo, cnt, bad);
+        if (a.groups <= 64) {
+            place = 0;
+            for (int o = 0; o < a.groups; ++o) {
+                const int c = __builtin_amdgcn_readlane(cnt, o);
+                place += c > cnt || (c == cnt && o < e);
+            }
+        }
+        order_g[place] = e;
+        order_first[place] = lo;
+        order_rows[place] = cnt;
+    }
+    if (bad && blockIdx.x == 0 && a.status) atomicOr(a.status, MEGA_MOE_STATUS_BAD_LAYOUT);
+    __syncthreads();
+    const int xcd = blockIdx.x & 7, total = a.groups * per;
+    int at = blockIdx.x >> 3;
+    const auto next = [&]() __attribute__((always_inline)) {
+        int nth = 0, li = 0, rows = 0;
+        bool found = false;
+        while (!found && at < total) {
+            nth = __builtin_amdgcn_readfirstlane(at / per);
+            li = __builtin_amdgcn_readfirstlane(xcd * per + at - nth * per);
+            at = __builtin_amdgcn_readfirstlane(at + kStreams);
+            rows = __builtin_amdgcn_readfirstlane(order_rows[nth]);
+            found = __builtin_amdgcn_readfirstlane(li < ntm * ntq && (rows > 0 || !a.accumulate));
+        }
+        const int g = __builtin_amdgcn_readfirstlane(order_g[nth]), first = __builtin_amdgcn_readfirstlane(order_first[nth]);
+        const int band = li / (8 * ntq), in = li - band * 8 * ntq, width = min(8, ntm - band * 8);
+        const int qt = in / width, m0 = (band * 8 + in - qt * width) * S::BM, q0 = qt * S::BN;
+        return S::of(found, a.p + (size_t)first * a.n, m0, a.q + (size_t)first * a.k, q0, rows,
+                     static_cast<char*>(a.out) + (((size_t)g * a.n + m0) * a.k + q0) * kBytes, a.n - m0, a.k - q0);
+    };
+    S::run(next, a.n, a.k, a.k, smem, wave, lane, [&](const char* p, bool exists, i32x4 v) {
+        if constexpr (kFp32)
+            if (a.accumulate && exists)
+                v = __builtin_bit_cast(i32x4, __builtin_bit_cast(f32x4, v) + *reinterpret_cast<const f32x4*>(p));
+        return v;
+    });
+}
+
 // dw = the parts added up in their order (dw += with accumulate); values is a multiple of 8
 template <class T, bool kFp32>
 __global__ __launch_bounds__(256) void grouped_join_kernel(const float* parts, int n_parts, size_t values, void* out,
@@ -154,6 +212,7 @@ int32_t check_grouped(const void* p, const void* q, const int32_t* off, const vo
 template <class L, class H, class T, bool kBackward, int BM, int BN>
 hipError_t launch_rows_with(const GroupedArgs& a, hipStream_t st) {
     const int64_t tiles = ((int64_t)a.rows / BM + min(a.groups, a.rows)) * (((kBackward ? a.k : a.n) + BN - 1) / BN);
+    if ((tiles + 7) * L::kThreads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((grouped_rows_kernel<L, H, T, kBackward, BM, BN>), dim3((uint32_t)((tiles + 7) / 8 * 8)),
                        dim3(L::kThreads), 0, st, a);
     return hipGetLastError();
@@ -208,8 +267,10 @@ int weight_parts(int64_t rows, int n, int k, int groups) {
 
 template <class T, bool kFp32>
 hipError_t launch_weight(GroupedArgs a, void* workspace, hipStream_t st) {
-    if (weight_tiles(a.n, a.k, a.groups, 256) >= kWeightLarge)
-        return launch_weight_with<QuadLoop<T, true, true, 256, 256, 2, 4>, T, kFp32, 256, 256>(a, st);
+    if (weight_tiles(a.n, a.k, a.groups, 256) >= kWeightLarge) {
+        hipLaunchKernelGGL((grouped_weight_stream_kernel<T, kFp32>), dim3(8 * kStreams), dim3(512), 0, st, a);
+        return hipGetLastError();
+    }
     using L = TileLoop<T, true, true, 128, 128, 2, 2, 2>;
     if (a.parts == 1) return launch_weight_with<L, T, kFp32, 128, 128>(a, st);
     void* dw = a.out;

@@ -688,7 +688,7 @@ bool one_group(int64_t pairs, int experts) { return pairs <= kOneGroupPairs && e
 int32_t check_router(const mega_moe_router_config* c) {
     if (!c || c->tokens < 0) return MEGA_MOE_ERR_INVALID_ARG;
     if (c->num_experts < 1 || c->num_experts > MEGA_MOE_MAX_EXPERTS || c->topk < 1 || c->topk > MEGA_MOE_MAX_TOPK ||
-        c->topk > c->num_experts || c->tokens >= (int64_t)1 << 31 || c->tokens * c->topk >= (int64_t)1 << 31 ||
+        c->topk > c->num_experts || c->tokens > MEGA_MOE_MAX_PAIRS || c->tokens * c->topk > MEGA_MOE_MAX_PAIRS ||
         (c->score != MEGA_MOE_SCORE_SOFTMAX && c->score != MEGA_MOE_SCORE_SIGMOID) || c->num_groups < 1 ||
         c->num_groups > 64 || c->num_experts % c->num_groups || c->topk_groups < 1 ||
         c->topk_groups > c->num_groups || (c->group_top != 1 && c->group_top != 2) ||
@@ -813,7 +813,7 @@ int32_t mega_moe_router_backward(const mega_moe_router_config* cfg, const float*
 
 int32_t mega_moe_group_workspace_bytes(int64_t pairs, int32_t num_local_experts, uint64_t* bytes_out) {
     if (!bytes_out || pairs < 0) return MEGA_MOE_ERR_INVALID_ARG;
-    if (pairs >= (int64_t)1 << 31 || num_local_experts < 1 || num_local_experts > MEGA_MOE_MAX_EXPERTS)
+    if (pairs > MEGA_MOE_MAX_PAIRS || num_local_experts < 1 || num_local_experts > MEGA_MOE_MAX_EXPERTS)
         return MEGA_MOE_ERR_UNSUPPORTED;
     const int64_t per = chunk_pairs(pairs);
     *bytes_out = one_group(pairs, num_local_experts) ? 0 : (uint64_t)((pairs + per - 1) / per + 1) * num_local_experts * 4;

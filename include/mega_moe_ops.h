@@ -33,6 +33,7 @@ extern "C" {
 
 #define MEGA_MOE_MAX_GROUP_ROWS (1 << 26)   /* rows of a grouped product or an adapter projection */
 #define MEGA_MOE_MAX_GROUP_COLS 65536       /* its n and k */
+#define MEGA_MOE_MAX_PAIRS 2147418112       /* 2^31 - 2^16: chosen (token, expert) pairs */
 #define MEGA_MOE_MAX_REQUESTS 4096          /* requests of an adapter projection */
 
 /* ------------------------------------------------------------------ products grouped by expert
@@ -76,7 +77,7 @@ int32_t mega_moe_grouped_weight_workspace_bytes(int64_t rows, int32_t n, int32_t
 #define MEGA_MOE_SCORE_SIGMOID 1   /* s = 1 / (1 + exp(-logit))                                       */
 
 typedef struct mega_moe_router_config {
-    int64_t tokens;        /* T: 0 .. 2^31-1; T * topk < 2^31                                          */
+    int64_t tokens;        /* T >= 0; T * topk at most MEGA_MOE_MAX_PAIRS                              */
     int32_t num_experts;   /* E: 1 .. MEGA_MOE_MAX_EXPERTS                                             */
     int32_t topk;          /* K: 1 .. min(E, MEGA_MOE_MAX_TOPK)                                        */
     int32_t score;         /* MEGA_MOE_SCORE_*                                                         */
@@ -124,7 +125,7 @@ int32_t mega_moe_router_backward(const mega_moe_router_config* cfg, const float*
  *              offsets[num_local_experts] on
  *   slot       int32 [pairs]: the place of pair p, -1 if it belongs to no group here
  *   workspace  mega_moe_group_workspace_bytes() bytes (may be NULL at 0); its contents do not matter
- * pairs 0 .. 2^31-1 (pointers of pair arrays may be NULL at 0); num_local_experts 1 .. MEGA_MOE_MAX_EXPERTS.
+ * pairs 0 .. MEGA_MOE_MAX_PAIRS (pointers of pair arrays may be NULL at 0); num_local_experts 1 .. MEGA_MOE_MAX_EXPERTS.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP. */
 int32_t mega_moe_group_workspace_bytes(int64_t pairs, int32_t num_local_experts, uint64_t* bytes_out /* host */);
 int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t first_expert,

@@ -146,10 +146,11 @@ def test_nan_stays_in_its_row_and_its_group():
     assert torch.isnan(dw[1]).all()
 
 
-@pytest.mark.parametrize("counts", [[30, 0, 200], [3000, 0, 2500]])
-def test_accumulate_into_fp32_gradient(counts):
-    x, dy, w, off_t, off = make(counts, 136, 264, torch.bfloat16, seed=7)
-    before = torch.randn(3, 136, 264, device="cuda")
+# one work-group per tile; parts of the rows; streams of tiles
+@pytest.mark.parametrize("counts,n,k", [([30, 0, 200], 136, 264), ([3000, 0, 2500], 136, 264), ([700, 0, 90], 2056, 2312)])
+def test_accumulate_into_fp32_gradient(counts, n, k):
+    x, dy, w, off_t, off = make(counts, n, k, torch.bfloat16, seed=7)
+    before = torch.randn(3, n, k, device="cuda")
     dw = before.clone()
     assert mm.grouped_backward_weight(dy, x, off_t, out=dw, accumulate=True) is dw
     check_weight(dy, x, off, dw, before)
@@ -201,7 +202,16 @@ def test_no_rows():
 
 
 def test_repeat_other_stream_and_graph_replay_give_the_same_bits():
-    x, dy, w, off_t, off = make([90, 0, 300, 11], 264, 392, torch.bfloat16, seed=10)
+    replay_all([90, 0, 300, 11], 264, 392)
+
+
+@pytest.mark.parametrize("counts,n,k", [([5000, 0, 2000], 264, 136), ([900, 1, 0, 2500, 40], 2056, 2056)])
+def test_split_sums_streams_and_large_tiles_replay_to_the_same_bits(counts, n, k):
+    replay_all(counts, n, k)
+
+
+def replay_all(counts, n, k):
+    x, dy, w, off_t, off = make(counts, n, k, torch.bfloat16, seed=10)
 
     def all_three(stream=None):
         return (mm.grouped_forward(x, w, off_t, stream=stream), mm.grouped_backward_rows(dy, w, off_t, stream=stream),

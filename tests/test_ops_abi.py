@@ -111,7 +111,7 @@ def test_ordering_refusals():
     out = ctypes.c_uint64(0)
     assert lib.mega_moe_group_workspace_bytes(10, 4, None) == mm.ERR_INVALID_ARG
     assert lib.mega_moe_group_workspace_bytes(-1, 4, ctypes.byref(out)) == mm.ERR_INVALID_ARG
-    for pairs, experts in ((1 << 31, 4), (10, 0), (10, 4097)):
+    for pairs, experts in ((1 << 31, 4), ((1 << 31) - 1, 4), (10, 0), (10, 4097)):
         assert lib.mega_moe_group_workspace_bytes(pairs, experts, ctypes.byref(out)) == mm.ERR_UNSUPPORTED
         assert lib.mega_moe_group_by_expert(P, pairs, 0, experts, P, P, P, P, 1 << 40, None) == mm.ERR_UNSUPPORTED
     need = mm.mega_moe_group_workspace_bytes(100000, 256)
