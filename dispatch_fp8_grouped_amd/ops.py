@@ -18,6 +18,7 @@ compute values and gradients and record no autograd graph.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import dispatch_fp8_grouped_amd as _mm       # the package imports this module last
 
@@ -140,6 +141,12 @@ def mega_moe_adapter_forward(x, w, a, b, scales, offsets, adapter, y, rows, n, k
 
 
 # --------------------------------------------------------------- checks
+# Sizes ask for the same workspace every time; the queries' ctypes calls would be a fifth of a small call's host time.
+_weight_bytes = functools.lru_cache(1024)(mega_moe_grouped_weight_workspace_bytes)
+_group_bytes = functools.lru_cache(1024)(mega_moe_group_workspace_bytes)
+_adapter_bytes = functools.lru_cache(1024)(mega_moe_adapter_workspace_bytes)
+
+
 def _want(name, t, shape, dtypes, device=None):
     """t is a dense GPU tensor of this shape and one of these types (shape None: any)."""
     if (t is not None and t.is_cuda and t.is_contiguous() and t.dtype in dtypes
@@ -193,7 +200,11 @@ def _halves():
     return _KINDS
 
 
-def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream, call):
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream):
     import torch
     kinds = _halves()
     _want("w", w, None, kinds)
@@ -206,12 +217,15 @@ def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream, call):
     _want("offsets", offsets, (groups + 1,), (torch.int32,), w.device)
     if status is not None:
         _want("status", status, (1,), (torch.int32,), w.device)
+    lib = _mm.lib()
+    call = lib.mega_moe_grouped_forward if contract_k else lib.mega_moe_grouped_backward_rows
     with _Call(w.device, stream) as raw:
         if out is None:
             out = torch.empty((rows, outer), dtype=w.dtype, device=w.device)
         else:
             _want("out", out, (rows, outer), (w.dtype,), w.device)
-        call(rows_in, w, offsets, out, rows, n, k, groups, kinds[w.dtype], status, raw)
+        _mm._check(call(rows_in.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(), rows, n, k, groups,
+                        kinds[w.dtype], _at(status), raw), what)
     return out
 
 
@@ -221,12 +235,12 @@ def grouped_forward(x, w, offsets, out=None, status=None, stream=None):
     x [rows, k], w [groups, n, k], both bfloat16 or float16; offsets int32 [groups + 1].  Rows that belong
     to no group are not written (in a new `out` they hold what the allocation held).  status: int32 [1], or
     None; see mega_moe_ops.h."""
-    return _grouped("grouped_forward", x, w, offsets, True, out, status, stream, mega_moe_grouped_forward)
+    return _grouped("grouped_forward", x, w, offsets, True, out, status, stream)
 
 
 def grouped_backward_rows(dy, w, offsets, out=None, status=None, stream=None):
     """dx[m] = dy[m] @ w[e]: the gradient of grouped_forward's rows.  dy [rows, n] -> dx [rows, k]."""
-    return _grouped("grouped_backward_rows", dy, w, offsets, False, out, status, stream, mega_moe_grouped_backward_rows)
+    return _grouped("grouped_backward_rows", dy, w, offsets, False, out, status, stream)
 
 
 def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=False, status=None, stream=None):
@@ -249,17 +263,21 @@ def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=Fal
         raise ValueError("accumulate needs a float32 `out`")
     if status is not None:
         _want("status", status, (1,), (torch.int32,), x.device)
-    nbytes = mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups)
+    nbytes = _weight_bytes(rows, n, k, groups)
     with _Call(x.device, stream) as raw:
         if out is None:
             out = torch.empty((groups, n, k), dtype=dtype, device=x.device)
         else:
             _want("out", out, (groups, n, k), (dtype,), x.device)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
-        mega_moe_grouped_backward_weight(dy, x, offsets, out, rows, n, k, groups, kinds[x.dtype],
-                                         FP32 if dtype == torch.float32 else kinds[dtype], accumulate, workspace, nbytes,
-                                         status, raw)
+        _mm._check(_mm.lib().mega_moe_grouped_backward_weight(
+            dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), out.data_ptr(), rows, n, k, groups, kinds[x.dtype],
+            FP32 if dtype == torch.float32 else kinds[dtype], 1 if accumulate else 0, _at(workspace), nbytes, _at(status),
+            raw), "grouped_backward_weight")
     return out
+
+
+_config = functools.lru_cache(1024)(mega_moe_router_config)
 
 
 def _router_config(logits, topk, score, num_groups, topk_groups, group_top, renormalize, scale):
@@ -271,8 +289,8 @@ def _router_config(logits, topk, score, num_groups, topk_groups, group_top, reno
         raise ValueError(f"score: want one of {sorted(_SCORES)}, got {score!r}")
     experts = logits.shape[-1]
     kind = FP32 if logits.dtype == torch.float32 else _halves()[logits.dtype]
-    return mega_moe_router_config(logits.numel() // experts, experts, topk, _SCORES[score], num_groups, topk_groups,
-                                  group_top, 1 if renormalize else 0, scale, kind)
+    return _config(logits.numel() // experts, experts, topk, _SCORES[score], num_groups, topk_groups, group_top,
+                   1 if renormalize else 0, scale, kind)
 
 
 def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_groups=1, group_top=1, renormalize=True,
@@ -291,7 +309,8 @@ def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_gro
     with _Call(logits.device, stream) as raw:
         idx = torch.empty(shape, dtype=torch.int64, device=logits.device)
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
-        mega_moe_router_topk(cfg, logits, bias, idx, weights, raw)
+        _mm._check(_mm.lib().mega_moe_router_topk(cfg, logits.data_ptr(), _at(bias), idx.data_ptr(), weights.data_ptr(),
+                                                  raw), "router_topk")
     return idx, weights
 
 
@@ -306,7 +325,8 @@ def router_backward(dweights, logits, topk_idx, score="softmax", renormalize=Tru
     _want("dweights", dweights, (*logits.shape[:-1], topk), (torch.float32,), logits.device)
     with _Call(logits.device, stream) as raw:
         dlogits = torch.empty_like(logits)
-        mega_moe_router_backward(cfg, dweights, logits, topk_idx, dlogits, raw)
+        _mm._check(_mm.lib().mega_moe_router_backward(cfg, dweights.data_ptr(), logits.data_ptr(), topk_idx.data_ptr(),
+                                                      dlogits.data_ptr(), raw), "router_backward")
     return dlogits
 
 
@@ -317,14 +337,15 @@ def group_by_expert(topk_idx, num_local_experts, first_expert=0, stream=None):
     import torch
     _want("topk_idx", topk_idx, None, (torch.int64,))
     pairs, device = topk_idx.numel(), topk_idx.device
-    nbytes = mega_moe_group_workspace_bytes(pairs, num_local_experts)
+    nbytes = _group_bytes(pairs, num_local_experts)
     with _Call(device, stream) as raw:
         offsets = torch.empty(num_local_experts + 1, dtype=torch.int32, device=device)
         order = torch.empty(pairs, dtype=torch.int32, device=device)
         slot = torch.empty(topk_idx.shape, dtype=torch.int32, device=device)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-        mega_moe_group_by_expert(topk_idx, pairs, first_expert, num_local_experts, offsets, order, slot, workspace,
-                                 nbytes, raw)
+        _mm._check(_mm.lib().mega_moe_group_by_expert(topk_idx.data_ptr(), pairs, first_expert, num_local_experts,
+                                                      offsets.data_ptr(), order.data_ptr(), slot.data_ptr(),
+                                                      _at(workspace), nbytes, raw), "group_by_expert")
     return offsets, order, slot
 
 
@@ -341,15 +362,16 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
         raise ValueError("adapter_forward: want x [rows, k], w [n, k], a [adapters, rank, k], adapter [requests]")
     n, k = w.shape
     rows, adapters, rank, requests = x.shape[0], a.shape[0], a.shape[1], adapter.shape[0]
-    for name, t, shape, types in (("x", x, (rows, k), (w.dtype,)), ("a", a, (adapters, rank, k), (w.dtype,)),
-                                  ("b", b, (adapters, n, rank), (w.dtype,)),
-                                  ("scales", scales, (adapters,), (torch.float32,)),
-                                  ("offsets", offsets, (requests + 1,), (torch.int32,)),
-                                  ("adapter", adapter, (requests,), (torch.int32,))):
-        _want(name, t, shape, types, w.device)
+    device, same = w.device, (w.dtype,)
+    _want("x", x, (rows, k), same, device)
+    _want("a", a, (adapters, rank, k), same, device)
+    _want("b", b, (adapters, n, rank), same, device)
+    _want("scales", scales, (adapters,), (torch.float32,), device)
+    _want("offsets", offsets, (requests + 1,), (torch.int32,), device)
+    _want("adapter", adapter, (requests,), (torch.int32,), device)
     if status is not None:
         _want("status", status, (1,), (torch.int32,), w.device)
-    nbytes = mega_moe_adapter_workspace_bytes(rows, n, k, rank, requests)
+    nbytes = _adapter_bytes(rows, n, k, rank, requests)
     with _Call(w.device, stream) as raw:
         if out is None:
             out = torch.empty((rows, n), dtype=w.dtype, device=w.device)
@@ -359,6 +381,8 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
         else:
             _want("workspace", workspace, None, (torch.uint8,), w.device)
-        mega_moe_adapter_forward(x, w, a, b, scales, offsets, adapter, out, rows, n, k, rank, requests, adapters,
-                                 kinds[w.dtype], workspace, None, status, raw)
+        _mm._check(_mm.lib().mega_moe_adapter_forward(
+            x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), offsets.data_ptr(), adapter.data_ptr(),
+            out.data_ptr(), rows, n, k, rank, requests, adapters, kinds[w.dtype], workspace.data_ptr(), workspace.numel(),
+            _at(status), raw), "adapter_forward")
     return out
