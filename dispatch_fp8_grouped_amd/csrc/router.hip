@@ -628,6 +628,8 @@ __global__ __launch_bounds__(256) void order_scan_kernel(OrderArgs a) {
 
 // 3: places.  Every work-group adds up the experts' totals for their first places.  Dynamic LDS: int [4][experts],
 // then int [4].
+// kShort: a wave has at most kPairsPerWave pairs, whose ids stay in registers.
+template <bool kShort>
 __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
     extern __shared__ int lds[];
     int* sums = lds + 4 * a.experts;
@@ -636,19 +638,34 @@ __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
     const int per = a.per_chunk / 4;
     const int64_t end = min(first + a.per_chunk, (int64_t)a.pairs);
     const int lo = (int)min(first + (int64_t)wave * per, end), hi = (int)min((int64_t)lo + per, end);
+    constexpr int kMine = kShort ? kPairsPerWave / 64 : 1;
+    int mine[kMine];
+    if constexpr (kShort)
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) mine[i] = lo + i * 64 + lane < hi ? local_of(a, lo + i * 64 + lane) : -1;
+    // the first batch of experts' places, on their way while the pairs are counted
+    const int* totals = a.hist + (size_t)a.experts * a.chunks;
+    int before = tid < a.experts ? a.hist[(size_t)tid * a.chunks + blockIdx.x] : 0, count = tid < a.experts ? totals[tid] : 0;
     for (int i = tid; i < 4 * a.experts; i += 256) lds[i] = 0;
     __syncthreads();
+    if constexpr (kShort) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (mine[i] >= 0) atomicAdd(&lds[wave * a.experts + mine[i]], 1);
+    } else {
 #pragma unroll 4
-    for (int p = lo + lane; p < hi; p += 64) {
-        const int e = local_of(a, p);
-        if (e >= 0) atomicAdd(&lds[wave * a.experts + e], 1);
+        for (int p = lo + lane; p < hi; p += 64) {
+            const int e = local_of(a, p);
+            if (e >= 0) atomicAdd(&lds[wave * a.experts + e], 1);
+        }
     }
-    __syncthreads();
     int base = 0;                                  // pairs of the experts before this batch of 256
     for (int e0 = 0; e0 < a.experts; e0 += 256) {
         const int e = e0 + tid;
-        const int before = e < a.experts ? a.hist[(size_t)e * a.chunks + blockIdx.x] : 0;
-        const int count = e < a.experts ? a.hist[(size_t)a.experts * a.chunks + e] : 0;
+        if (e0) {
+            before = e < a.experts ? a.hist[(size_t)e * a.chunks + blockIdx.x] : 0;
+            count = e < a.experts ? totals[e] : 0;
+        }
         const int incl = wave_prefix(count, lane);
         if (lane == 63) sums[wave] = incl;
         __syncthreads();
@@ -662,6 +679,7 @@ __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
         if (e < a.experts) {
             if (blockIdx.x == 0) a.offsets[e] = start;
             int at = start + before;
+#pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const int c = lds[w * a.experts + e];
                 lds[w * a.experts + e] = at;
@@ -673,8 +691,14 @@ __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
     }
     if (blockIdx.x == 0 && tid == 0) a.offsets[a.experts] = base;
     const int bits = bits_of(a.experts);
-    for (int p0 = lo; p0 < hi; p0 += 64)
-        place_pairs(a, a.order, p0 + lane < hi ? local_of(a, p0 + lane) : -1, p0 + lane, hi, lds + wave * a.experts, bits);
+    if constexpr (kShort) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (lo + i * 64 < hi) place_pairs(a, a.order, mine[i], lo + i * 64 + lane, hi, lds + wave * a.experts, bits);
+    } else {
+        for (int p0 = lo; p0 < hi; p0 += 64)
+            place_pairs(a, a.order, p0 + lane < hi ? local_of(a, p0 + lane) : -1, p0 + lane, hi, lds + wave * a.experts, bits);
+    }
     for (int64_t i = max(first, (int64_t)base) + tid; i < end; i += 256) a.order[i] = -1;
 }
 
@@ -844,7 +868,9 @@ int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t
     const dim3 chunks(a.chunks), block(256);
     hipLaunchKernelGGL(order_count_kernel, chunks, block, num_local_experts * sizeof(int), st, a);
     hipLaunchKernelGGL(order_scan_kernel, dim3((num_local_experts + 3) / 4), block, 0, st, a);
-    hipLaunchKernelGGL(order_place_kernel, chunks, block, (4 * num_local_experts + 4) * sizeof(int), st, a);
+    const size_t lds = (4 * num_local_experts + 4) * sizeof(int);
+    if (a.per_chunk <= 4 * kPairsPerWave) hipLaunchKernelGGL(order_place_kernel<true>, chunks, block, lds, st, a);
+    else hipLaunchKernelGGL(order_place_kernel<false>, chunks, block, lds, st, a);
     return hipGetLastError() == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
