@@ -3,13 +3,13 @@
 //
 // Choice: LANES lanes per token (a wave, or a quarter of one); lane l of them holds experts l*EPL .. l*EPL + EPL-1
 // (so the lowest lane of a tie holds the lowest expert).  Without a bias the logit and the expert's number make one
-// fp64 number, all different: each lane sorts its own once, and a round is a maximum over the lanes' first ones.  With
-// a bias the fp64 score + bias is the rank, as two unsigned words: a round takes the largest high word, and only
-// where several lanes share it do the low words decide.  What bounds it is instruction issue (about
-// 1000 a wave), and the rounds cost the same whether a wave serves one token or four, so many tokens take a quarter
-// wave each: 32768 tokens x 256 experts, top 8, bf16, 38 us with a wave each and 16 with a quarter (the bytes: 5).
-// Few tokens take a whole wave, whose lanes have fewer experts to walk (1024 x 256, fp32, sigmoid with bias and
-// groups: 8 us).
+// key, all different: each lane sorts its own once, and a round is a maximum over the lanes' first ones.  With a bias
+// the fp64 score + bias is the rank, as two unsigned words: a round takes the largest high word, and only where
+// several lanes share it do the low words decide.  What bounds it is instruction issue, and the rounds cost the same
+// whether a wave serves one token or four, so many tokens take a quarter wave each.  32768 tokens x 256 experts,
+// top 8, bf16: 38 us with a wave each and fp64 keys, 16 with a quarter, 11.5 with 32-bit keys, both loads in flight
+// and the chosen logits taken from the keys (the bytes: 5).  Few tokens take a whole wave, whose lanes have fewer
+// experts to walk (1024 x 256, fp32, sigmoid with bias and groups: 8 us).
 //
 // Scores are computed in fp64 (exp of the C library's device functions): two scores that differ in fp32
 // logits then differ in rank, and the choice does not hang on a rounding of exp.
@@ -83,12 +83,15 @@ __device__ __forceinline__ void read_lane(const V* row, int E, int lane, float (
     struct __align__(kWide * sizeof(V)) Wide { V v[kWide]; };
     const int e0 = lane * EPL;
     if (E % EPL == 0) {
+        // lanes behind the row read its last values, and drop them: no branch between the loads
+        const Wide* from = reinterpret_cast<const Wide*>(row + min(e0, E - EPL));
+        Wide w[EPL / kWide];
 #pragma unroll
-        for (int j = 0; j < EPL; j += kWide) {
-            Wide w{};
-            if (e0 < E) w = *reinterpret_cast<const Wide*>(row + e0 + j);
+        for (int j = 0; j < EPL / kWide; ++j) w[j] = from[j];
 #pragma unroll
-            for (int i = 0; i < kWide; ++i) x[j + i] = e0 < E ? value(w.v[i]) : -__builtin_inff();
+        for (int j = 0; j < EPL; ++j) {
+            const float v = value(w[j / kWide].v[j % kWide]);
+            x[j] = e0 < E ? v : -__builtin_inff();
         }
     } else {
 #pragma unroll
@@ -110,22 +113,56 @@ __device__ __forceinline__ void read_row(const void* p, int type, int64_t t, int
 __device__ __forceinline__ bool is_masked(float x) { return !(x > -__builtin_inff()); }
 __device__ __forceinline__ float clip_inf(float x) { return fminf(x, 3.402823466e38f); }
 
-// A logit and its expert as one fp64 number: the logit takes 24 of the 53 bits, the expert's number goes into the
-// low 12, so that of equal logits the lower expert's number is larger.  All are different and above -inf.
-__device__ __forceinline__ double with_expert(float x, int e) {
-    const uint64_t u = (uint64_t)__double_as_longlong((double)(x + 0.0f));        // -0 ranks with +0
-    return __longlong_as_double((long long)(u | (uint64_t)(u >> 63 ? e : MEGA_MOE_MAX_EXPERTS - 1 - e)));
-}
-__device__ __forceinline__ int expert_of(double key) {
-    const uint64_t u = (uint64_t)__double_as_longlong(key);
-    const int low = (int)(u & (MEGA_MOE_MAX_EXPERTS - 1));
-    return u >> 63 ? low : MEGA_MOE_MAX_EXPERTS - 1 - low;
-}
+// A logit and its expert as one number, so that of equal logits the lower expert's number is larger; all are
+// different, and above kNone unless the logit is masked.  fp32: an fp64 number, of whose 53 bits the logit takes 24
+// and the expert the low 12.  bf16 and fp16: their values as fp32 end with 12 zeros at least, which the expert takes;
+// unsigned integers in the order of the numbers cost half the registers and less than half the instructions.
+constexpr int kExpertMask = MEGA_MOE_MAX_EXPERTS - 1;
 static_assert(MEGA_MOE_MAX_EXPERTS == 1 << 12, "12 bits");
+template <class Key>
+struct Ranked;
+template <>
+struct Ranked<double> {
+    static constexpr double kNone = -__builtin_inff();
+    static __device__ __forceinline__ double of(float x, int e) {
+        const uint64_t u = (uint64_t)__double_as_longlong((double)(clip_inf(x) + 0.0f));        // -0 ranks with +0
+        const double key = __longlong_as_double((long long)(u | (uint64_t)(u >> 63 ? e : kExpertMask - e)));
+        return is_masked(x) ? kNone : key;
+    }
+    static __device__ __forceinline__ int expert(double key) {
+        const uint64_t u = (uint64_t)__double_as_longlong(key);
+        const int low = (int)(u & kExpertMask);
+        return u >> 63 ? low : kExpertMask - low;
+    }
+    static __device__ __forceinline__ float logit(double key) {
+        return (float)__longlong_as_double(__double_as_longlong(key) & ~(long long)kExpertMask);
+    }
+};
+template <>
+struct Ranked<uint32_t> {
+    static constexpr uint32_t kNone = 0x007FFFFFu;                 // -inf with any expert is not above it
+    static __device__ __forceinline__ uint32_t of(float x, int e) {
+        const uint32_t u = __float_as_uint(fmaxf(x, -__builtin_inff()) + 0.0f);                 // NaN becomes -inf
+        return ((u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) & ~(uint32_t)kExpertMask) + (uint32_t)(kExpertMask - e);
+    }
+    static __device__ __forceinline__ int expert(uint32_t key) { return kExpertMask - (int)(key & kExpertMask); }
+    static __device__ __forceinline__ float logit(uint32_t key) {
+        return __uint_as_float((key >> 31 ? key ^ 0x80000000u : ~key) & ~(uint32_t)kExpertMask);
+    }
+};
+template <>
+struct Ranked<uint64_t> {
+    static constexpr uint64_t kNone = 0;
+};
+
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint32_t smaller(uint32_t a, uint32_t b) { return min(a, b); }
 
 // Sort n numbers, the largest first (Batcher's odd-even merge network; n a power of two)
-template <int n>
-__device__ __forceinline__ void sort_down(double (&v)[n]) {
+template <int n, class Key>
+__device__ __forceinline__ void sort_down(Key (&v)[n]) {
 #pragma unroll
     for (int p = 1; p < n; p *= 2)
 #pragma unroll
@@ -135,9 +172,9 @@ __device__ __forceinline__ void sort_down(double (&v)[n]) {
 #pragma unroll
                 for (int i = 0; i < k; ++i)
                     if (i + j + k < n && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
-                        const double a = v[i + j], b = v[i + j + k];
-                        v[i + j] = fmax(a, b);
-                        v[i + j + k] = fmin(a, b);
+                        const Key a = v[i + j], b = v[i + j + k];
+                        v[i + j] = larger(a, b);
+                        v[i + j + k] = smaller(a, b);
                     }
 }
 
@@ -151,7 +188,7 @@ __device__ __forceinline__ uint64_t order64(double x) {
 // permutations and mirrors; the row and half-wave swaps return both halves)
 template <int kCtrl>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, true);
 }
 template <int d>
 __device__ __forceinline__ uint32_t mirror(uint32_t v) {
@@ -240,10 +277,12 @@ __device__ __forceinline__ void merge_top2(double& a, double& b, double c, doubl
     a = hi;
 }
 
-// kWide: ranks as two words (with a bias, or with too many experts to a lane to sort).  A work-group's tokens
-// follow each other.
-template <int EPL, int LANES, bool kSigmoid, bool kWide, bool kGroups, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1) void router_kernel(RouterArgs a) {
+// Key: a logit with its expert as double or uint32_t (with_expert), or uint64_t for ranks as two words without
+// the expert (with a bias, or with too many experts to a lane to sort).  A work-group's tokens follow each other.
+template <int EPL, int LANES, bool kSigmoid, class Key, bool kGroups, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, (EPL <= 16 && !std::is_same<Key, uint64_t>::value && !kGroups ? 4 : 1)) void
+router_kernel(RouterArgs a) {
+    constexpr bool kWide = std::is_same<Key, uint64_t>::value;
     constexpr int kTokens = WAVES * 64 / LANES;
     __shared__ double values[kGroups ? kTokens : 1][kGroups ? EPL * LANES : 1];
     const int lane = threadIdx.x % LANES, mine = threadIdx.x / LANES, wave = threadIdx.x >> 6;
@@ -259,29 +298,32 @@ __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             live[j] = !is_masked(x[j]);
-            x[j] = clip_inf(x[j]);
-            if (live[j]) top = fmaxf(top, x[j]);
+            if constexpr (kWide) x[j] = clip_inf(x[j]);
         }
         // softmax needs its largest logit and its sum where the scores themselves enter the result; where they
         // are divided by the chosen ones' sum both cancel
         const bool by_score = (kWide && a.bias) || (kGroups && a.gtop == 2);
         double total = 1.0;
         if (!kSigmoid && (by_score || !a.renorm)) {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                if (live[j]) top = fmaxf(top, clip_inf(x[j]));
             top = max_of<LANES>(top);              // -inf where everything is masked
             total = 0.0;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
-                if (live[j]) total += exp((double)x[j] - (double)top);
+                if (live[j]) total += exp((double)clip_inf(x[j]) - (double)top);
             total = sum_of<LANES>(total);
         }
         uint32_t hi[kWide ? EPL : 1], lo[kWide ? EPL : 1];
-        double key[kWide ? 1 : EPL];
+        Key key[kWide ? 1 : EPL];
+        constexpr Key none_key = Ranked<Key>::kNone;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = lane * EPL + j;
             double rank = x[j], worth = x[j];
             if (by_score && live[j]) {
-                const double s = kSigmoid ? sigmoid64(x[j]) : exp((double)x[j] - (double)top) / total;
+                const double s = kSigmoid ? sigmoid64(x[j]) : exp((double)clip_inf(x[j]) - (double)top) / total;
                 worth = s;
                 if (kWide && a.bias) {
                     worth = rank = s + (double)a.bias[e];
@@ -293,7 +335,7 @@ __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1
                 hi[j] = (uint32_t)(word >> 32);
                 lo[j] = (uint32_t)word;
             } else {
-                key[j] = live[j] ? with_expert(x[j], e) : none;
+                key[j] = Ranked<Key>::of(x[j], e);
             }
             if constexpr (kGroups) values[mine][e] = live[j] ? worth : none;
         }
@@ -334,13 +376,14 @@ __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1
                 const int e = lane * EPL + j, at = e < a.E ? e / size * L : 0;
                 if (!((kept >> at) & 1)) {
                     if constexpr (kWide) hi[j] = lo[j] = 0;
-                    else key[j] = none;
+                    else key[j] = none_key;
                 }
             }
             __builtin_amdgcn_wave_barrier();
         }
         // K rounds; lane k keeps choice k
         int chosen = -1;
+        float chosen_x = -__builtin_inff();
         if constexpr (kWide) {
             // a live rank's high word is never 0
             for (int k = 0; k < a.K; ++k) {
@@ -371,21 +414,28 @@ __global__ __launch_bounds__(WAVES * 64, EPL <= 16 && !kWide && !kGroups ? 4 : 1
             // every lane's experts sorted once: a round looks at the lanes' first ones, and the lane that had the
             // largest moves up.  Only the first K of a lane can be reached.
             sort_down(key);
+            Key mine_key = none_key;
             auto rounds = [&](auto depth) {
                 constexpr int kDepth = decltype(depth)::value;
                 for (int k = 0; k < a.K; ++k) {
-                    const double best = max_of<LANES>(key[0]);
-                    if (lane == k && best > none) chosen = expert_of(best);
+                    const Key best = max_of<LANES>(key[0]);
+                    if (lane == k) mine_key = best;
                     const bool mine_won = key[0] == best;
 #pragma unroll
-                    for (int j = 0; j < kDepth; ++j) key[j] = mine_won ? (j + 1 < EPL ? key[j + 1 < EPL ? j + 1 : 0] : none) : key[j];
+                    for (int j = 0; j < kDepth; ++j) {
+                        const Key next = j + 1 < EPL ? key[j + 1 < EPL ? j + 1 : 0] : none_key, now = key[j];
+                        key[j] = mine_won ? next : now;
+                    }
                 }
             };
             if (EPL > 8 && a.K <= 8) rounds(std::integral_constant<int, EPL < 8 ? EPL : 8>{});
             else rounds(std::integral_constant<int, EPL>{});
+            if (mine_key > none_key) {
+                chosen = Ranked<Key>::expert(mine_key);
+                chosen_x = clip_inf(Ranked<Key>::logit(mine_key));
+            }
         }
-        // the chosen logit once more, from the cache
-        float chosen_x = chosen >= 0 ? clip_inf(read_value(a.logits, a.type, (size_t)t * a.E + chosen)) : -__builtin_inff();
+        if (kWide && chosen >= 0) chosen_x = clip_inf(read_value(a.logits, a.type, (size_t)t * a.E + chosen));   // from the cache
         // renormalized, softmax's common factor cancels: taken relative to the largest chosen logit, the sum
         // cannot underflow where a bias or the groups left the largest logits out
         if (!kSigmoid && a.renorm) {
@@ -424,6 +474,8 @@ __global__ __launch_bounds__(WAVES * 64) void router_backward_kernel(RouterArgs 
     for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 + wave * (64 / LANES) < a.tokens; t0 += (int64_t)gridDim.x * kTokens) {
         const bool real = t0 + mine < a.tokens;
         const int64_t t = real ? t0 + mine : a.tokens - 1;
+        float x[kAll ? EPL : 1];
+        if constexpr (kAll) read_row<EPL>(a.logits, a.type, t, a.E, lane, x);
         int64_t id = -1;
         float g = 0.f, xk = -__builtin_inff();
         if (lane < a.K) {
@@ -439,8 +491,6 @@ __global__ __launch_bounds__(WAVES * 64) void router_backward_kernel(RouterArgs 
         float top;
         double total = 1.0;
         if constexpr (kAll) {
-            float x[EPL];
-            read_row<EPL>(a.logits, a.type, t, a.E, lane, x);
             top = -__builtin_inff();
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
@@ -628,7 +678,7 @@ __global__ __launch_bounds__(256) void order_scan_kernel(OrderArgs a) {
 
 // 3: places.  Every work-group adds up the experts' totals for their first places.  Dynamic LDS: int [4][experts],
 // then int [4].
-// kShort: a wave has at most kPairsPerWave pairs, whose ids stay in registers.
+// kShort: a wave has at most kPairsPerWave pairs, whose ids stay in registers (262144 pairs: 7.4 us against 8.0).
 template <bool kShort>
 __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
     extern __shared__ int lds[];
@@ -740,27 +790,30 @@ uint32_t router_grid(int64_t tokens, int per) {
     return (uint32_t)(g < (1 << 20) ? g : 1 << 20);
 }
 
-template <int EPL, int LANES, bool kSigmoid, bool kWide, bool kGroups>
+template <int EPL, int LANES, bool kSigmoid, class Key, bool kGroups>
 hipError_t launch_router(const RouterArgs& a, hipStream_t st) {
     // the groups' values take EPL * 512 bytes of LDS per wave
     constexpr int WAVES = kGroups && EPL > 16 ? 1 : 4;
-    hipLaunchKernelGGL((router_kernel<EPL, LANES, kSigmoid, kWide, kGroups, WAVES>),
+    hipLaunchKernelGGL((router_kernel<EPL, LANES, kSigmoid, Key, kGroups, WAVES>),
                        dim3(router_grid(a.tokens, WAVES * 64 / LANES)), dim3(WAVES * 64), 0, st, a);
     return hipGetLastError();
 }
+template <int EPL, int LANES, class Key>
+hipError_t pick_form(const RouterArgs& a, bool sigmoid, hipStream_t st) {
+    switch ((sigmoid ? 2 : 0) | (a.G > 1 ? 1 : 0)) {
+        case 0: return launch_router<EPL, LANES, false, Key, false>(a, st);
+        case 1: return launch_router<EPL, LANES, false, Key, true>(a, st);
+        case 2: return launch_router<EPL, LANES, true, Key, false>(a, st);
+        default: return launch_router<EPL, LANES, true, Key, true>(a, st);
+    }
+}
 template <int EPL, int LANES>
 hipError_t pick_router(const RouterArgs& a, bool sigmoid, hipStream_t st) {
-    constexpr bool kWalk = EPL > 16;               // always as words
-    switch ((sigmoid ? 4 : 0) | (a.bias || kWalk ? 2 : 0) | (a.G > 1 ? 1 : 0)) {
-        case 0: return launch_router<EPL, LANES, false, kWalk, false>(a, st);
-        case 1: return launch_router<EPL, LANES, false, kWalk, true>(a, st);
-        case 2: return launch_router<EPL, LANES, false, true, false>(a, st);
-        case 3: return launch_router<EPL, LANES, false, true, true>(a, st);
-        case 4: return launch_router<EPL, LANES, true, kWalk, false>(a, st);
-        case 5: return launch_router<EPL, LANES, true, kWalk, true>(a, st);
-        case 6: return launch_router<EPL, LANES, true, true, false>(a, st);
-        default: return launch_router<EPL, LANES, true, true, true>(a, st);
+    if constexpr (EPL <= 16) {
+        if (!a.bias && a.type == MEGA_MOE_FP32) return pick_form<EPL, LANES, double>(a, sigmoid, st);
+        if (!a.bias) return pick_form<EPL, LANES, uint32_t>(a, sigmoid, st);
     }
+    return pick_form<EPL, LANES, uint64_t>(a, sigmoid, st);
 }
 template <int EPL, int LANES>
 hipError_t pick_backward(const RouterArgs& a, bool sigmoid, hipStream_t st) {

@@ -384,3 +384,27 @@ def test_a_layer_from_its_router_to_its_gradients():
                            ("dlogits", dlogits, L.grad)):
         d = (got.double().cpu() - ref).abs().max().item()
         assert d <= 8 * 2.0 ** -8 * ref.abs().max().item(), (name, d, ref.abs().max().item())
+
+
+def test_sixteen_bit_ranks():
+    """bf16 and fp16 ranks: every sign, infinities beside the largest finite numbers, subnormal numbers, both
+    zeros and NaN of both signs; 16 lanes and 64 lanes per token."""
+    for kind in (torch.bfloat16, torch.float16):
+        bits = torch.arange(65536, device="cuda", dtype=torch.int32).to(torch.int16)
+        values = bits.view(kind)
+        order = torch.randperm(65536, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+        mixed = values[order].view(256, 256)
+        for t in (256, 4096):
+            x = mixed.repeat(t // 256, 1).contiguous()
+            print(f"[case] {kind} {t}", flush=True)
+            idx, _ = mm.router_topk(x, 16, score="sigmoid", renormalize=False)
+            wide = x.double()
+            wide = torch.where(torch.isnan(wide), torch.full_like(wide, -float("inf")), wide)
+            want = torch.sort(wide, dim=1, descending=True, stable=True)[1][:, :16]
+            assert torch.equal(idx.cpu(), want.cpu())
+
+
+def test_ordering_of_many_pairs_for_a_wave():
+    """More pairs than the ordering's waves hold in registers."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    check_order(torch.randint(-1, 300, ((1 << 20) + 777,), device="cuda", generator=g), 257)
