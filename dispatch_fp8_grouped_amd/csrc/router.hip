@@ -21,8 +21,8 @@ namespace mm {
 namespace {
 
 constexpr int kPairsPerWave = 256;           // least pairs that one wave of the ordering places, 64 at a time
-constexpr int kOneGroupPairs = 8192;         // up to here one work-group orders everything in one launch
-constexpr int kOneGroupExperts = 256;       // 16 KB of counters beside 32 KB of places
+constexpr int kFewPairs = 32768;             // up to here one launch orders everything
+constexpr int kFewExperts = 512;             // 36 KB of counters
 
 struct RouterArgs {
     const void* logits;
@@ -556,10 +556,10 @@ struct OrderArgs {
     int pairs, first, experts, chunks, per_chunk;   // per_chunk pairs per work-group
 };
 
-__device__ __forceinline__ int local_of(const OrderArgs& a, int p) {
-    const int64_t e = a.idx[p];
+__device__ __forceinline__ int local_id(const OrderArgs& a, int64_t e) {
     return e >= a.first && e < (int64_t)a.first + a.experts ? (int)(e - a.first) : -1;
 }
+__device__ __forceinline__ int local_of(const OrderArgs& a, int p) { return local_id(a, a.idx[p]); }
 
 // Lanes of the wave with the same expert as this one (experts < 4096: 12 bits).
 __device__ __forceinline__ uint64_t same_expert(int e, int bits) {
@@ -576,12 +576,12 @@ __device__ __forceinline__ uint64_t same_expert(int e, int bits) {
 
 // Places of 64 consecutive pairs, one wave: lane's pair p goes to expert e (-1: none); `next` (LDS, the wave's
 // own) holds the next free place of every expert.
-__device__ __forceinline__ void place_pairs(const OrderArgs& a, int32_t* order, int e, int p, int hi, int* next, int bits) {
+__device__ __forceinline__ void place_pairs(const OrderArgs& a, int e, int p, int hi, int* next, int bits) {
     const uint64_t same = same_expert(e, bits);
     int place = -1;
     if (e >= 0) {
         place = next[e] + __popcll(same & lanemask_lt());
-        order[place] = p;
+        a.order[place] = p;
     }
     __builtin_amdgcn_wave_barrier();
     if (e >= 0 && (same & lanemask_lt()) == 0) next[e] = place + __popcll(same);
@@ -591,43 +591,51 @@ __device__ __forceinline__ void place_pairs(const OrderArgs& a, int32_t* order, 
 
 __device__ __forceinline__ int bits_of(int experts) { return experts > 1 ? 32 - __clz(experts - 1) : 0; }
 
-// Few pairs: everything in one work-group of 16 waves, each with up to 512 consecutive pairs.  The places are put
-// together in LDS and stored in order (8192 pairs, 256 experts: 11 us, against 16 for the three launches below).
-// Dynamic LDS: int [16][experts], int [17 rounded to 32], int [pairs].
-__global__ __launch_bounds__(1024) void order_small_kernel(OrderArgs a) {
+// Few pairs, one launch: every work-group counts all pairs and places 1024 of them, 64 to a wave, so that nothing
+// passes between work-groups (8192 pairs, 256 experts: 6.0 us; one work-group placing all of them 11, the three
+// launches below 10; at 32768 pairs 10.2 against 10.5).  Dynamic LDS: int [16][experts] its own waves' counts, [experts] of the pairs before its
+// own, [experts] of those behind, [32].
+__global__ __launch_bounds__(1024) void order_few_kernel(OrderArgs a) {
     extern __shared__ int lds[];
-    int* sums = lds + 16 * a.experts;
-    int* order = sums + 32;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int per = ((a.pairs + 15) / 16 + 63) / 64 * 64;
-    const int lo = min(wave * per, a.pairs), hi = min(lo + per, a.pairs);
-    int mine[kOneGroupPairs / 1024];               // all ids in flight at once
-#pragma unroll
-    for (int i = 0; i < kOneGroupPairs / 1024; ++i) mine[i] = lo + i * 64 + lane < hi ? local_of(a, lo + i * 64 + lane) : -1;
-    for (int i = tid; i < 16 * a.experts; i += 1024) lds[i] = 0;
+    int *before = lds + 16 * a.experts, *behind = before + a.experts, *sums = behind + a.experts;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, own = blockIdx.x, p = own * 1024 + tid;
+    for (int i = tid; i < 18 * a.experts; i += 1024) lds[i] = 0;
     __syncthreads();
+    int mine = -1;
+    for (int c0 = 0; c0 < a.pairs; c0 += 8 * 1024) {
+        int64_t id[8];                             // in flight at once
 #pragma unroll
-    for (int i = 0; i < kOneGroupPairs / 1024; ++i)
-        if (mine[i] >= 0) atomicAdd(&lds[wave * a.experts + mine[i]], 1);
+        for (int i = 0; i < 8; ++i) id[i] = a.idx[min(c0 + i * 1024 + tid, a.pairs - 1)];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = c0 / 1024 + i, e = c * 1024 + tid < a.pairs ? local_id(a, id[i]) : -1;
+            if (c == own) mine = e;
+            if (e >= 0) atomicAdd(&(c < own ? before : c > own ? behind : lds + wave * a.experts)[e], 1);
+        }
+    }
     __syncthreads();
-    // thread e: the expert's total (experts <= 256), then an exclusive prefix over the experts
-    int count = 0;
-    if (tid < a.experts)
+    // thread e: the expert's total (experts <= 512), then an exclusive prefix over the experts
+    int count = 0, earlier = 0;
+    if (tid < a.experts) {
+        earlier = before[tid];
+        count = earlier + behind[tid];
 #pragma unroll
         for (int w = 0; w < 16; ++w) count += lds[w * a.experts + tid];
+    }
     const int incl = wave_prefix(count, lane);
     if (lane == 63) sums[wave] = incl;
     __syncthreads();
-    if (wave == 0) {
-        const int v = lane < 16 ? sums[lane] : 0;
-        const int s = wave_prefix(v, lane);
-        if (lane < 16) sums[lane] = s - v;
-        if (lane == 15) sums[16] = s;
+    int first = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        const int v = sums[w];
+        first += w < wave ? v : 0;
+        all += v;
     }
-    __syncthreads();
     if (tid < a.experts) {
-        int at = sums[wave] + incl - count;
-        a.offsets[tid] = at;
+        const int start = first + incl - count;
+        if (own == 0) a.offsets[tid] = start;
+        int at = start + earlier;
 #pragma unroll
         for (int w = 0; w < 16; ++w) {
             const int c = lds[w * a.experts + tid];
@@ -635,15 +643,10 @@ __global__ __launch_bounds__(1024) void order_small_kernel(OrderArgs a) {
             at += c;
         }
     }
-    const int all = sums[16];
-    if (tid == 0) a.offsets[a.experts] = all;
+    if (own == 0 && tid == 0) a.offsets[a.experts] = all;
     __syncthreads();
-    const int bits = bits_of(a.experts);
-#pragma unroll
-    for (int i = 0; i < kOneGroupPairs / 1024; ++i)
-        if (lo + i * 64 < hi) place_pairs(a, order, mine[i], lo + i * 64 + lane, hi, lds + wave * a.experts, bits);
-    __syncthreads();
-    for (int i = tid; i < a.pairs; i += 1024) a.order[i] = i < all ? order[i] : -1;
+    place_pairs(a, mine, p, a.pairs, lds + wave * a.experts, bits_of(a.experts));
+    if (p >= all && p < a.pairs) a.order[p] = -1;
 }
 
 // Many pairs, three launches.  1: every chunk's counts, hist[expert][chunk].  Dynamic LDS: int [experts].
@@ -744,10 +747,10 @@ __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
     if constexpr (kShort) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
-            if (lo + i * 64 < hi) place_pairs(a, a.order, mine[i], lo + i * 64 + lane, hi, lds + wave * a.experts, bits);
+            if (lo + i * 64 < hi) place_pairs(a, mine[i], lo + i * 64 + lane, hi, lds + wave * a.experts, bits);
     } else {
         for (int p0 = lo; p0 < hi; p0 += 64)
-            place_pairs(a, a.order, p0 + lane < hi ? local_of(a, p0 + lane) : -1, p0 + lane, hi, lds + wave * a.experts, bits);
+            place_pairs(a, p0 + lane < hi ? local_of(a, p0 + lane) : -1, p0 + lane, hi, lds + wave * a.experts, bits);
     }
     for (int64_t i = max(first, (int64_t)base) + tid; i < end; i += 256) a.order[i] = -1;
 }
@@ -757,7 +760,7 @@ int64_t chunk_pairs(int64_t pairs) {
     const int64_t least = 4 * kPairsPerWave, by_chunks = (pairs + 1023) / 1024;
     return ((by_chunks < least ? least : by_chunks) + 255) / 256 * 256;
 }
-bool one_group(int64_t pairs, int experts) { return pairs <= kOneGroupPairs && experts <= kOneGroupExperts; }
+bool few_pairs(int64_t pairs, int experts) { return pairs <= kFewPairs && experts <= kFewExperts; }
 
 int32_t check_router(const mega_moe_router_config* c) {
     if (!c || c->tokens < 0) return MEGA_MOE_ERR_INVALID_ARG;
@@ -893,7 +896,7 @@ int32_t mega_moe_group_workspace_bytes(int64_t pairs, int32_t num_local_experts,
     if (pairs > MEGA_MOE_MAX_PAIRS || num_local_experts < 1 || num_local_experts > MEGA_MOE_MAX_EXPERTS)
         return MEGA_MOE_ERR_UNSUPPORTED;
     const int64_t per = chunk_pairs(pairs);
-    *bytes_out = one_group(pairs, num_local_experts) ? 0 : (uint64_t)((pairs + per - 1) / per + 1) * num_local_experts * 4;
+    *bytes_out = few_pairs(pairs, num_local_experts) ? 0 : (uint64_t)((pairs + per - 1) / per + 1) * num_local_experts * 4;
     return MEGA_MOE_OK;
 }
 
@@ -911,8 +914,9 @@ int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t
     hipStream_t st = static_cast<hipStream_t>(stream);
     OrderArgs a{topk_idx, offsets, order, slot, static_cast<int32_t*>(workspace), (int)pairs, first_expert,
                 num_local_experts, 0, 0};
-    if (one_group(pairs, num_local_experts)) {
-        hipLaunchKernelGGL(order_small_kernel, dim3(1), dim3(1024), (16 * num_local_experts + 32 + pairs) * sizeof(int), st, a);
+    if (few_pairs(pairs, num_local_experts)) {
+        hipLaunchKernelGGL(order_few_kernel, dim3((uint32_t)(pairs > 1024 ? (pairs + 1023) / 1024 : 1)), dim3(1024),
+                           (18 * num_local_experts + 32) * sizeof(int), st, a);
         return hipGetLastError() == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
     }
     a.per_chunk = (int)chunk_pairs(pairs);

@@ -408,3 +408,10 @@ def test_ordering_of_many_pairs_for_a_wave():
     """More pairs than the ordering's waves hold in registers."""
     g = torch.Generator(device="cuda").manual_seed(4)
     check_order(torch.randint(-1, 300, ((1 << 20) + 777,), device="cuda", generator=g), 257)
+
+
+@pytest.mark.parametrize("pairs", [1023, 1024, 1025, 9 * 1024 + 1, 32767, 32768, 32769])
+def test_ordering_at_the_edges_of_its_work_groups(pairs):
+    g = torch.Generator(device="cuda").manual_seed(pairs)
+    for experts in (3, 512, 513):
+        check_order(torch.randint(-1, experts + 2, (pairs,), device="cuda", generator=g), experts)
