@@ -4,6 +4,14 @@
 //   backward_weight  dw[e] = dy_e^T x_e       P = dy columns (KS), Q = x columns (KS), contraction rows
 // The row-major weights are read as they are in all three: where the contraction runs down the memory rows
 // the fragments are transposed on their way out of LDS.
+//
+// Measured, bf16.  Many rows (32768 x 4096 x 7168 over 32 groups): 1.69 ms, 1140 TFLOP/s.  The loop itself reaches 1430
+// where one group fills its tiles (8192 rows, 335 us); the rest goes to the groups' last tiles, to the ninth and tenth
+// round of tiles on 256 CUs, and to the clock, which the DMA's power takes from 2.17 to 1.89 GHz.  Few rows stream the
+// weights: 1024 x 7168 x 2048 over 32 groups 171 us (5.6 TB/s), eight rows for eight groups of 4096 x 7168 78 us (6.0).
+// The gradient of rows (8192 rows, 32 x 4096 x 1536: 148 us, 700 TFLOP/s, 3.3 TB/s) has the forward's bounds, and both
+// at once.  The gradient of weights of short groups writes as much as it multiplies, and the two share the CUs' time:
+// 16384 rows, 32 x 4096 x 7168, fp32, 1.39 ms for 962 GFLOP and 4.1 GB.
 #include <type_traits>
 
 #include "gemm_kernels.h"
@@ -251,8 +259,8 @@ hipError_t launch_weight_with(const GroupedArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// 256 x 256 tiles where they fill the CUs (16384 rows, 32 x 4096 x 7168, fp32: 1.44 ms against 1.75 with
-// 128 x 128).  Below that the smaller ones, four times as many, and where these leave CUs without work and the
+// 256 x 256 tiles where they fill the CUs (16384 rows, 32 x 4096 x 7168, fp32: 1.39 ms as streams of tiles, 1.44 with a
+// work-group for each, 1.75 with 128 x 128).  Below that the smaller ones, four times as many, and where these leave CUs without work and the
 // groups are long, the rows are split into parts of at least four steps (of an average group) that a second launch adds up.
 constexpr int kWeightLarge = 192;
 int64_t weight_tiles(int n, int k, int groups, int edge) {
