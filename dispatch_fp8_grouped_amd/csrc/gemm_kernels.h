@@ -511,7 +511,10 @@ inline int pick_row_shape(int rows, int cols, int depth, int groups, int choices
         double row_tiles = groups == 1 ? (rows + s.bm - 1) / s.bm : (double)rows / s.bm + 0.5 * used;
         if (row_tiles < used) row_tiles = used;
         const double tiles = row_tiles * ((cols + s.bn - 1) / s.bn), rounds = tiles / (256.0 * s.resident);
-        const double per_step = tiles <= 256 ? s.alone : s.full * (rounds > 1 ? (double)(int64_t)(rounds + 0.95) : 1.0);
+        // one group's tiles are counted exactly, and one more than a round holds starts another; the count of several is
+        // an estimate, and their short last tiles soften the step
+        const double whole = (double)(int64_t)(rounds + (groups == 1 ? 1.0 - 1e-9 : 0.95));
+        const double per_step = tiles <= 256 ? s.alone : s.full * (rounds > 1 ? whole : 1.0);
         const double t = s.fixed + steps * per_step;
         if (i == 0 || t < least) {
             least = t;
