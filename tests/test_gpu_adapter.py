@@ -41,7 +41,9 @@ def check(s, y, rows=None):
         dv = (k + 1) * 2.0 ** -24 * sv + (eps / 2) ** 2 * v.abs() + tiny / 2
         want[m] += v @ bt
         bound[m] += dv @ bt.abs() + 2 * rank * 2.0 ** -24 * ((v.abs() + dv) @ bt.abs()) * 1.01
-        bound[m] += 2.0 ** -24 * (want[m].abs() + bound[m])       # the adapter's sum added to the shared one
+        # the adapter's 2 rank terms are added onto the shared sum, each addition rounding a partial sum of at most S1 + S2
+        bound[m] += 2 * rank * 2.0 ** -24 * (x[m].abs() @ wt.abs()) * 1.01
+        bound[m] += 2.0 ** -24 * (want[m].abs() + bound[m])       # or, with few rows, its own sum added to it
     bound = bound + eps / 2 * (want.abs() + bound) + tiny / 2
     sel = slice(None) if rows is None else rows
     d = (y.double() - want)[sel].abs()
@@ -164,3 +166,21 @@ def test_repeat_other_stream_and_graph_replay_give_the_same_bits():
         eager = mm.adapter_forward(**s)
         for o in outs:
             assert torch.equal(o, eager), i
+
+
+def test_rows_past_32_bit_offsets():
+    rows, n, k, rank = 540_000, 4104, 16, 8
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x = torch.randn(rows, k, generator=g, device="cuda").bfloat16()
+    w = torch.randn(n, k, generator=g, device="cuda").bfloat16()
+    a = torch.randn(2, rank, k, generator=g, device="cuda").bfloat16()
+    b = torch.randn(2, n, rank, generator=g, device="cuda").bfloat16()
+    scales = torch.tensor([0.5, -2.0], device="cuda")
+    off = torch.tensor([0, 300_001, 530_000, rows], dtype=torch.int32, device="cuda")
+    which = torch.tensor([1, -1, 0], dtype=torch.int32, device="cuda")
+    y = mm.adapter_forward(x, w, a, b, scales, off, which)
+    assert y.numel() > 2 ** 31
+    for i, m in ((1, slice(0, 200)), (1, slice(299_900, 300_001)), (-1, slice(300_001, 300_200)), (-1, slice(529_900, 530_000)),
+                 (0, slice(530_000, 530_200)), (0, slice(rows - 100, rows))):
+        check(dict(x=x[m], w=w, a=a, b=b, scales=scales, offsets=torch.tensor([0, m.stop - m.start]), adapter=torch.tensor([i])),
+              y[m])

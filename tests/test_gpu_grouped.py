@@ -238,3 +238,69 @@ def replay_all(counts, n, k):
         eager = all_three()
         for a, b in zip(eager, got):
             assert torch.equal(a, b), i
+
+
+def test_row_tensors_past_32_bit_offsets():
+    """Rows of more than 2^32 bytes and 2^31 values, in one group and at the edge of another."""
+    rows, n, k = 600_000, 16, 4104
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.randn(rows, k, generator=g, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn(rows, n, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(2, n, k, generator=g, device="cuda", dtype=torch.bfloat16)
+    off = [0, 590_001, rows]
+    off_t = torch.tensor(off, dtype=torch.int32, device="cuda")
+    y = mm.grouped_forward(x, w, off_t)
+    dx = mm.grouped_backward_rows(dy, w, off_t)
+    for e, s in ((0, slice(0, 300)), (0, slice(523_000, 523_500)), (0, slice(589_800, 590_001)), (1, slice(590_001, 590_300)),
+                 (1, slice(rows - 100, rows))):
+        a, d, b = x[s].double(), dy[s].double(), w[e].double()
+        bt = b.t().contiguous()
+        close(y[s], a @ bt, a.abs() @ bt.abs(), k)
+        close(dx[s], d @ b, d.abs() @ b.abs(), n)
+    dw = mm.grouped_backward_weight(dy, x, off_t, dtype=torch.float32)
+    for e in range(2):
+        want, mag = torch.zeros(n, k, device="cuda", dtype=torch.float64), torch.zeros(n, k, device="cuda", dtype=torch.float64)
+        for r in range(off[e], off[e + 1], 50_000):
+            s = slice(r, min(r + 50_000, off[e + 1]))
+            a, b = dy[s].double().t().contiguous(), x[s].double()
+            want += a @ b
+            mag += a.abs() @ b.abs()
+        close(dw[e], want, mag, off[e + 1] - off[e])
+
+
+def test_weights_past_32_bit_offsets():
+    groups, n, k = 40, 8192, 8200
+    counts = [3, 0, 1] + [0] * 35 + [2, 5]
+    g = torch.Generator(device="cuda").manual_seed(12)
+    off = offsets_of(counts)
+    off_t = torch.tensor(off, dtype=torch.int32, device="cuda")
+    x = torch.randn(off[-1], k, generator=g, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn(off[-1], n, generator=g, device="cuda", dtype=torch.bfloat16)
+    dw = mm.grouped_backward_weight(dy, x, off_t)
+    assert dw.numel() > 2 ** 31
+    for e in (0, 1, 2, 20, 38, 39):
+        a, b = dy[off[e]:off[e + 1]].double().t().contiguous(), x[off[e]:off[e + 1]].double()
+        close(dw[e], a @ b, a.abs() @ b.abs(), counts[e] + 1)
+    y, dx = mm.grouped_forward(x, dw, off_t), mm.grouped_backward_rows(dy, dw, off_t)
+    for e in (0, 2, 38, 39):
+        s = slice(off[e], off[e + 1])
+        a, d, b = x[s].double(), dy[s].double(), dw[e].double()
+        bt = b.t().contiguous()
+        close(y[s], a @ bt, a.abs() @ bt.abs(), k)
+        close(dx[s], d @ b, d.abs() @ b.abs(), n)
+
+
+def test_two_calls_at_once_on_two_streams():
+    x, dy, w, off_t, off = make([900, 1, 0, 2500, 40], 2056, 2056, torch.bfloat16, seed=13)
+    x2, dy2, w2, off2_t, off2 = make([5000, 0, 2000], 264, 136, torch.bfloat16, seed=14)
+    want = (mm.grouped_forward(x, w, off_t), mm.grouped_backward_weight(dy, x, off_t, dtype=torch.float32))
+    want2 = (mm.grouped_forward(x2, w2, off2_t), mm.grouped_backward_weight(dy2, x2, off2_t, dtype=torch.float32))
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = (mm.grouped_forward(x, w, off_t, stream=one), mm.grouped_backward_weight(dy, x, off_t, dtype=torch.float32, stream=one))
+        got2 = (mm.grouped_forward(x2, w2, off2_t, stream=two),
+                mm.grouped_backward_weight(dy2, x2, off2_t, dtype=torch.float32, stream=two))
+        torch.cuda.synchronize()
+        for a, b in zip(want + want2, got + got2):
+            assert torch.equal(a, b)

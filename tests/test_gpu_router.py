@@ -415,3 +415,21 @@ def test_ordering_at_the_edges_of_its_work_groups(pairs):
     g = torch.Generator(device="cuda").manual_seed(pairs)
     for experts in (3, 512, 513):
         check_order(torch.randint(-1, experts + 2, (pairs,), device="cuda", generator=g), experts)
+
+
+def test_logits_past_32_bit_offsets():
+    """More than 2^31 logits: the last tokens as a call for them alone gives them."""
+    t, e = 8_500_000, 256
+    x = torch.empty(t, e, device="cuda", dtype=torch.bfloat16)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    for r in range(0, t, 500_000):
+        x[r:r + 500_000] = torch.randn(min(500_000, t - r), e, generator=g, device="cuda").bfloat16()
+    idx, w = mm.router_topk(x, 4)
+    for s in (slice(0, 5000), slice(t - 5000, t)):
+        some = x[s].contiguous()
+        i, v = mm.router_topk(some, 4)
+        assert torch.equal(i, idx[s]) and torch.equal(v, w[s])
+    dw = torch.randn(t, 4, generator=g, device="cuda")
+    d = mm.router_backward(dw, x, idx)
+    for s in (slice(0, 5000), slice(t - 5000, t)):
+        assert torch.equal(d[s], mm.router_backward(dw[s].contiguous(), x[s].contiguous(), idx[s].contiguous()))
