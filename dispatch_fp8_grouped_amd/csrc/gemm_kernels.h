@@ -488,6 +488,8 @@ struct KsStream {
 // at 512 x 512 x 512 over 4 groups 14.4, 9.8, 7.3, 6.1, 5.4, 6.1, 8.3 us; at 1024 x 7168 x 2048 over 32 groups
 // (weights streamed) 183, 175, 170, 188, 202, 240, 194 us; at 64 x 4096 x 7168, one group, 70, 52, 48, 35, 28, 19,
 // 53 us; at 1500 x 2048 x 4096 over 4 groups 80, 48, 46, 69, 82, 84, 38 us.
+// Over 44 sizes drawn from 4 to 32768 rows, 1 to 64 groups and 128 to 8192 columns, both directions, the shape picked took
+// 1.9 % longer than the best of them on average and 17 % at most.
 struct RowShape {
     int bm, bn, resident;
     double fixed, alone, full;
