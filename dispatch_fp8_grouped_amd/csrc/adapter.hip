@@ -17,8 +17,8 @@
 // error of half a step of the 16-bit type to every v; the second number takes it to 2^-16 (bf16) for twice the
 // (few) operations of the second product.
 //
-// Measured, bf16.  64 requests of one row, rank 16, 4096 x 7168: 29 us for 68 MB (parts 22, join 7): bound by the
-// weights' stream, which has 20 us to ramp up and drain, and the latency of two launches.  8192 rows of 12 requests,
+// Measured, bf16.  64 requests of one row, rank 16, 4096 x 7168: 22 us for 68 MB (parts 16, join 7): bound by the
+// weights' stream, which has 16 us to ramp up and drain, and the latency of two launches.  8192 rows of 12 requests,
 // rank 64, 4096 x 7168: 404 us, 1210 TFLOP/s (down 25, bound by one read of x; up 380, bound by the MFMAs; with b's
 // fragments read again for every 16 rows the whole took 420).  One row, rank 32, 7168 x 2048: 15 us, of which the host
 // takes most.
@@ -56,20 +56,23 @@ __device__ __forceinline__ Operand part_of(const uint16_t* p, int extent, int k,
     return Operand{p + k0, extent, k, max(min(k - k0, steps * kStepK), 0)};
 }
 
-constexpr int kDownM = 64, kDownN = 64, kPartM = 64, kPartN = 128;
+constexpr int kDownM = 64, kFewDownM = 32, kDownN = 64, kPartM = 64, kPartN = 128;
 template <class T>
 using DownLoop = TileLoop<T, false, false, kDownM, kDownN, 2, 2, 3>;
+// A request of few rows is bound by the latency of one step after the other: four stages in flight
+template <class T>
+using FewDownLoop = TileLoop<T, false, false, kFewDownM, kDownN, 2, 2, 4>;
 template <class T>
 using PartLoop = TileLoop<T, false, false, kPartM, kPartN, 1, 4, 3>;
 
 // One tile of u for one part of the contraction; block counts the down tiles times the parts.
-template <class T>
+template <class L>
 __device__ __forceinline__ void down_tile(const AdapterArgs& g, int block, uint8_t* smem, int wave, int lane) {
-    using L = DownLoop<T>;
+    constexpr int kM = L::kRows;
     if (block == 0 && g.status)
         for (int r = threadIdx.x; r < g.requests; r += L::kThreads)
             if (g.adapter[r] < -1 || g.adapter[r] >= g.adapters) atomicOr(g.status, MEGA_MOE_STATUS_BAD_EXPERT_ID);
-    const TileMap<kDownM> map(g.off, g.requests, g.rows, (g.rank + kDownN - 1) / kDownN, 8, lane,
+    const TileMap<kM> map(g.off, g.requests, g.rows, (g.rank + kDownN - 1) / kDownN, 8, lane,
                               block ? nullptr : g.status);
     const int part = block % g.u_parts, tile = block / g.u_parts;
     if (tile >= map.total) return;
@@ -77,7 +80,7 @@ __device__ __forceinline__ void down_tile(const AdapterArgs& g, int block, uint8
     if (t.g < 0) return;
     const int ad = __builtin_amdgcn_readfirstlane(adapter_of(g, t.g));
     if (ad < 0) return;
-    const int m0 = t.mt * kDownM, c0 = t.nt * kDownN;
+    const int m0 = t.mt * kM, c0 = t.nt * kDownN;
     const Operand P = part_of(g.x + (size_t)(t.lo + m0) * g.k, t.cnt - m0, g.k, part, g.u_steps);
     const Operand Q = part_of(g.a + ((size_t)ad * g.rank + c0) * g.k, g.rank - c0, g.k, part, g.u_steps);
     typename L::Acc acc[L::QI][L::MI];
@@ -96,21 +99,22 @@ template <class T>
 __global__ __launch_bounds__(256) void adapter_down_kernel(AdapterArgs g) {
     static_assert(DownLoop<T>::kThreads == 256, "one launch");
     __shared__ __align__(1024) uint8_t smem[DownLoop<T>::kLds];
-    down_tile<T>(g, blockIdx.x, smem, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), threadIdx.x & 63);
+    down_tile<DownLoop<T>>(g, blockIdx.x, smem, __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), threadIdx.x & 63);
 }
 
 // Few rows: work-groups 0 .. shared - 1 the parts of the shared product, then the rows' adapters, then the down tiles
 template <class T>
 __global__ __launch_bounds__(256) void adapter_parts_kernel(AdapterArgs g, int shared) {
     using L = PartLoop<T>;
-    static_assert(L::kThreads == 256 && DownLoop<T>::kThreads == 256, "one launch");
-    __shared__ __align__(1024) uint8_t smem[L::kLds > DownLoop<T>::kLds ? L::kLds : DownLoop<T>::kLds];
+    using Down = FewDownLoop<T>;
+    static_assert(L::kThreads == 256 && Down::kThreads == 256, "one launch");
+    __shared__ __align__(1024) uint8_t smem[L::kLds > Down::kLds ? L::kLds : Down::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int block = blockIdx.x;
     if (block >= shared) {
         block -= shared;
         if (block > 0) {
-            down_tile<T>(g, block - 1, smem, wave, lane);
+            down_tile<Down>(g, block - 1, smem, wave, lane);
             return;
         }
         for (int m = threadIdx.x; m < g.rows; m += 256) {
@@ -175,8 +179,11 @@ __device__ __forceinline__ void low_rank_row(const AdapterArgs& g, int m, int c,
         }
 }
 
-// Few rows: a wave per 16 x 16 block of y adds up the parts and its rows' adapters.
-template <class T>
+// Few rows: a wave per 16 x 16 block of y adds up the parts and its rows' adapters.  It is bound by the latency of its
+// loads: the parts' are on their way while the adapters are looked up, and the b of kAtOnce adapters are read together.
+// 16 where requests have few rows (64 rows with 24 adapters, rank 16: 6.4 us a launch, 7.2 with eight at a time, 9.8 with
+// four and the parts first), 4 with half the registers where neighbouring rows share theirs.
+template <class T, int kAtOnce>
 __global__ __launch_bounds__(256) void adapter_join_kernel(AdapterArgs g) {
     const int lane = threadIdx.x & 63, col_blocks = (g.n + 15) / 16;
     const int block = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
@@ -184,45 +191,47 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(AdapterArgs g) {
     const int m0 = block / col_blocks * 16, n0 = block % col_blocks * 16;
     const int m = min(m0 + (lane & 15), g.rows - 1), n = n0 + (lane >> 4) * 4;
     const int ad = g.requests > 0 ? g.of_row[m] : -1;
+    constexpr int kParts = 8;
+    const float* p = g.part + (size_t)m * g.n + min(n, g.n - 4);
+    f32x4 part[kParts];
+#pragma unroll
+    for (int s = 0; s < kParts; ++s) part[s] = *reinterpret_cast<const f32x4*>(p + (size_t)min(s, g.y_parts - 1) * g.rows * g.n);
     f32x4 sum{0.f, 0.f, 0.f, 0.f};
-    if (n < g.n) {
-        const float* p = g.part + (size_t)m * g.n + n;
-#pragma unroll 8
-        for (int s = 0; s < g.y_parts; ++s) sum += *reinterpret_cast<const f32x4*>(p + (size_t)s * g.rows * g.n);
-    }
     uint32_t left = (uint32_t)__ballot(ad >= 0) & 0xFFFFu;        // rows whose adapter is still to be added
-    if (left) {
-        const float scale = ad >= 0 ? g.scales[ad] : 0.f;
-        const int nq = min(n0 + (lane & 15), g.n - 1), kq = (lane >> 4) * 8;
-        while (left) {
-            // four adapters at a time, so that their loads are in flight together
-            int id[4];
+    const float scale = ad >= 0 ? g.scales[ad] : 0.f;
+    const int nq = min(n0 + (lane & 15), g.n - 1), kq = (lane >> 4) * 8;
+    while (left) {
+        int id[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                id[i] = left ? __builtin_amdgcn_readlane(ad, __ffs(left) - 1) : -1;
-                left &= ~(uint32_t)__ballot(ad == id[i]);
-            }
-            f32x4 delta[4] = {};
-            for (int c0 = 0; c0 < g.rank; c0 += 32) {
-                const int c = c0 + kq;
-                i32x4 q[4], hi, lo;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    q[i] = row_chunk(g.b + ((size_t)max(id[i], 0) * g.n + nq) * g.rank, c, id[i] >= 0 ? g.rank : 0);
-                // a row without an adapter has no u: its lanes stay at zero
-                low_rank_row<T>(g, m, ad >= 0 ? c : g.rank, scale, hi, lo);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    delta[i] = T::mfma(q[i], hi, delta[i]);
-                    delta[i] = T::mfma(q[i], lo, delta[i]);
-                }
-            }
-            // only its own rows: another request's infinity must not reach a row by way of 0 * inf
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (id[i] >= 0) sum += ad == id[i] ? delta[i] : f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < kAtOnce; ++i) {
+            id[i] = left ? __builtin_amdgcn_readlane(ad, __ffs(left) - 1) : -1;
+            left &= ~(uint32_t)__ballot(ad == id[i]);
         }
+        f32x4 delta[kAtOnce] = {};
+        for (int c0 = 0; c0 < g.rank; c0 += 32) {
+            const int c = c0 + kq;
+            i32x4 q[kAtOnce], hi, lo;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                q[i] = row_chunk(g.b + ((size_t)max(id[i], 0) * g.n + nq) * g.rank, c, id[i] >= 0 ? g.rank : 0);
+            // a row without an adapter has no u: its lanes stay at zero
+            low_rank_row<T>(g, m, ad >= 0 ? c : g.rank, scale, hi, lo);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                delta[i] = T::mfma(q[i], hi, delta[i]);
+                delta[i] = T::mfma(q[i], lo, delta[i]);
+            }
+        }
+        // only its own rows: another request's infinity must not reach a row by way of 0 * inf
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (id[i] >= 0) sum += ad == id[i] ? delta[i] : f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    f32x4 shared = part[0];
+#pragma unroll
+    for (int s = 1; s < kParts; ++s) shared += s < g.y_parts ? part[s] : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = kParts; s < g.y_parts; ++s) shared += *reinterpret_cast<const f32x4*>(p + (size_t)s * g.rows * g.n);
+    sum += shared;
     if (m0 + (lane & 15) < g.rows && n < g.n)
         *reinterpret_cast<u32x2*>(g.y + (size_t)m * g.n + n) = u32x2{T::pack(sum[0], sum[1]), T::pack(sum[2], sum[3])};
 }
@@ -314,18 +323,37 @@ Plan plan_of(int rows, int n, int k, int rank, int requests) {
     Plan p{};
     const int steps = (k + kStepK - 1) / kStepK;
     p.few = rows <= kFewRows;
-    const auto split = [&](int64_t tiles, int most, int& parts, int& per) {
-        // a work-group to a CU where the launch has others beside them, else two (64 requests, 4096 x 7168: 30 us
-        // against 34 the other way, parts and joining launch together), and at least four steps to a part, whose
-        // pipeline is three deep
-        parts = clamp((p.few ? 256 : 512) / (tiles > 0 ? tiles : 1), 1, clamp(steps / 4, 1, most));
+    p.u_tiles = requests > 0 ? ((int64_t)rows / (p.few ? kFewDownM : kDownM) + (requests < rows ? requests : rows)) * ((rank + kDownN - 1) / kDownN) : 0;
+    p.y_tiles = (int64_t)((rows + kPartM - 1) / kPartM) * ((n + kPartN - 1) / kPartN);
+    // at least four steps to a part, whose pipeline is three deep
+    const int most = clamp(steps / 4, 1, 8);
+    const int64_t u_tiles = p.u_tiles > 0 ? p.u_tiles : 1;
+    if (p.few) {
+        // two work-groups to a CU at once, down tiles and shared tiles together; the longest part as short as that
+        // allows, a step of either taking about as long, then the other's, then few parts to join (64 requests, 4096 x
+        // 7168: 5 parts of u and 5 or 6 of y 24.4 us, 4 and 8 26.0, 6 and 4 25.6, 8 and 8 31.6)
+        int least = 0;
+        for (int y = 1; y <= 2 * most; ++y) {
+            const int64_t left = 512 - p.y_tiles * y;
+            if (y > 1 && left < p.u_tiles) break;
+            const int u = clamp(left / u_tiles, 1, most), u_len = p.u_tiles > 0 ? (steps + u - 1) / u : 0, y_len = (steps + y - 1) / y;
+            const int cost = 4 * (u_len > y_len ? u_len : y_len) + (u_len < y_len ? u_len : y_len) + y;
+            if (y == 1 || cost < least) {
+                least = cost;
+                p.u_parts = u;
+                p.y_parts = y;
+            }
+        }
+    } else {
+        p.u_parts = clamp(512 / u_tiles, 1, most);
+        p.y_parts = 1;
+    }
+    const auto even = [&](int& parts, int& per) {
         per = (steps + parts - 1) / parts;
         parts = (steps + per - 1) / per;
     };
-    p.u_tiles = requests > 0 ? ((int64_t)rows / kDownM + (requests < rows ? requests : rows)) * ((rank + kDownN - 1) / kDownN) : 0;
-    split(p.u_tiles, 8, p.u_parts, p.u_steps);
-    p.y_tiles = (int64_t)((rows + kPartM - 1) / kPartM) * ((n + kPartN - 1) / kPartN);
-    split(p.y_tiles, 16, p.y_parts, p.y_steps);
+    even(p.u_parts, p.u_steps);
+    even(p.y_parts, p.y_steps);
     const auto up = [](uint64_t v) { return (v + 255) / 256 * 256; };
     p.part_at = up((uint64_t)p.u_parts * rows * rank * 4);
     p.row_at = p.part_at + (p.few ? up((uint64_t)p.y_parts * rows * n * 4) : 0);
@@ -347,7 +375,10 @@ hipError_t launch_adapter(const AdapterArgs& g, const Plan& p, hipStream_t st) {
         hipLaunchKernelGGL((adapter_parts_kernel<T>), dim3((uint32_t)(shared + 1 + p.u_tiles * p.u_parts)), dim3(256), 0, st, g,
                            shared);
         const int blocks = (g.rows + 15) / 16 * ((g.n + 15) / 16);
-        hipLaunchKernelGGL((adapter_join_kernel<T>), dim3((blocks + 3) / 4), dim3(256), 0, st, g);
+        if (g.requests > 4 && g.rows < 4 * g.requests)
+            hipLaunchKernelGGL((adapter_join_kernel<T, 16>), dim3((blocks + 3) / 4), dim3(256), 0, st, g);
+        else
+            hipLaunchKernelGGL((adapter_join_kernel<T, 4>), dim3((blocks + 3) / 4), dim3(256), 0, st, g);
         return hipGetLastError();
     }
     if (p.u_tiles > 0)
