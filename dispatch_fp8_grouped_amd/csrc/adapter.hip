@@ -20,8 +20,8 @@
 // Measured, bf16.  64 requests of one row, rank 16, 4096 x 7168: 22 us for 68 MB (parts 16, join 7): bound by the
 // weights' stream, which has 16 us to ramp up and drain, and the latency of two launches.  8192 rows of 12 requests,
 // rank 64, 4096 x 7168: 404 us, 1210 TFLOP/s (down 25, bound by one read of x; up 380, bound by the MFMAs; with b's
-// fragments read again for every 16 rows the whole took 420).  One row, rank 32, 7168 x 2048: 15 us, of which the host
-// takes most.
+// fragments read again for every 16 rows the whole took 420).  One row, rank 32, 7168 x 2048: 10 us replayed from
+// a graph, 15 from the host, whose call takes as long.
 #include <type_traits>
 
 #include "gemm_kernels.h"
@@ -30,6 +30,7 @@ namespace mm {
 namespace {
 
 constexpr int kFewRows = 256;
+constexpr int kMostParts = 8;          // of u
 
 struct AdapterArgs {
     const uint16_t *x, *w, *a, *b;
@@ -154,15 +155,32 @@ __device__ __forceinline__ i32x4 row_chunk(const uint16_t* row, int c, int cols)
     return c < cols ? *reinterpret_cast<const i32x4*>(row + c) : i32x4{0, 0, 0, 0};
 }
 
-// scale * u[m][c .. c+7] (the parts added in their order) as hi and lo; zeros from column `rank` on
-template <class T>
+// scale * u[m][c .. c+7] (the parts added in their order) as hi and lo; zeros from column `rank` on.  kTogether: the
+// loads of up to kMostParts parts go out before the first is needed (parts that do not exist repeat the last).
+template <class T, bool kTogether>
 __device__ __forceinline__ void low_rank_row(const AdapterArgs& g, int m, int c, float scale, i32x4& hi, i32x4& lo) {
     f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     if (c < g.rank) {
         const float* u = g.u + (size_t)m * g.rank + c;
-        for (int s = 0; s < g.u_parts; ++s, u += (size_t)g.rows * g.rank) {
-            v[0] += *reinterpret_cast<const f32x4*>(u);
-            v[1] += *reinterpret_cast<const f32x4*>(u + 4);
+        if constexpr (kTogether) {
+            f32x4 part[kMostParts][2];
+#pragma unroll
+            for (int s = 0; s < kMostParts; ++s) {
+                const float* at = u + (size_t)min(s, g.u_parts - 1) * g.rows * g.rank;
+                part[s][0] = *reinterpret_cast<const f32x4*>(at);
+                part[s][1] = *reinterpret_cast<const f32x4*>(at + 4);
+            }
+#pragma unroll
+            for (int s = 0; s < kMostParts; ++s)
+                if (s < g.u_parts) {
+                    v[0] += part[s][0];
+                    v[1] += part[s][1];
+                }
+        } else {
+            for (int s = 0; s < g.u_parts; ++s, u += (size_t)g.rows * g.rank) {
+                v[0] += *reinterpret_cast<const f32x4*>(u);
+                v[1] += *reinterpret_cast<const f32x4*>(u + 4);
+            }
         }
     }
 #pragma unroll
@@ -182,8 +200,10 @@ __device__ __forceinline__ void low_rank_row(const AdapterArgs& g, int m, int c,
 // Few rows: a wave per 16 x 16 block of y adds up the parts and its rows' adapters.  It is bound by the latency of its
 // loads: the parts' are on their way while the adapters are looked up, and the b of kAtOnce adapters are read together.
 // 16 where requests have few rows (64 rows with 24 adapters, rank 16: 6.4 us a launch, 7.2 with eight at a time, 9.8 with
-// four and the parts first), 4 with half the registers where neighbouring rows share theirs.
-template <class T, int kAtOnce>
+// four and the parts first), 4 with half the registers where neighbouring rows share theirs.  kTogether for few blocks,
+// which have no other waves to hide the reads of u behind: one row, rank 256, 4096 x 7168 23 us against 37 for the whole
+// call; with 4096 blocks the registers cost more than that (256 rows of one request, rank 256: 84 against 50).
+template <class T, int kAtOnce, bool kTogether>
 __global__ __launch_bounds__(256) void adapter_join_kernel(AdapterArgs g) {
     const int lane = threadIdx.x & 63, col_blocks = (g.n + 15) / 16;
     const int block = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
@@ -215,7 +235,7 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(AdapterArgs g) {
             for (int i = 0; i < kAtOnce; ++i)
                 q[i] = row_chunk(g.b + ((size_t)max(id[i], 0) * g.n + nq) * g.rank, c, id[i] >= 0 ? g.rank : 0);
             // a row without an adapter has no u: its lanes stay at zero
-            low_rank_row<T>(g, m, ad >= 0 ? c : g.rank, scale, hi, lo);
+            low_rank_row<T, kTogether>(g, m, ad >= 0 ? c : g.rank, scale, hi, lo);
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
                 delta[i] = T::mfma(q[i], hi, delta[i]);
@@ -281,7 +301,7 @@ __device__ __forceinline__ void up_tile(const AdapterArgs& g, int m0, int q0, ui
                 // not reach a row by way of 0 * inf
                 const bool mine = m >= lo && m < lo + cnt;
                 i32x4 hi, lo16;
-                low_rank_row<T>(g, min(m, g.rows - 1), mine ? c : g.rank, scale, hi, lo16);
+                low_rank_row<T, false>(g, min(m, g.rows - 1), mine ? c : g.rank, scale, hi, lo16);
 #pragma unroll
                 for (int i = 0; i < L::QI; ++i) {
                     const f32x4 sum = T::mfma(q[i], lo16, T::mfma(q[i], hi, acc[i][j]));
@@ -326,7 +346,7 @@ Plan plan_of(int rows, int n, int k, int rank, int requests) {
     p.u_tiles = requests > 0 ? ((int64_t)rows / (p.few ? kFewDownM : kDownM) + (requests < rows ? requests : rows)) * ((rank + kDownN - 1) / kDownN) : 0;
     p.y_tiles = (int64_t)((rows + kPartM - 1) / kPartM) * ((n + kPartN - 1) / kPartN);
     // at least four steps to a part, whose pipeline is three deep
-    const int most = clamp(steps / 4, 1, 8);
+    const int most = clamp(steps / 4, 1, kMostParts);
     const int64_t u_tiles = p.u_tiles > 0 ? p.u_tiles : 1;
     if (p.few) {
         // two work-groups to a CU at once, down tiles and shared tiles together; the longest part as short as that
@@ -375,10 +395,10 @@ hipError_t launch_adapter(const AdapterArgs& g, const Plan& p, hipStream_t st) {
         hipLaunchKernelGGL((adapter_parts_kernel<T>), dim3((uint32_t)(shared + 1 + p.u_tiles * p.u_parts)), dim3(256), 0, st, g,
                            shared);
         const int blocks = (g.rows + 15) / 16 * ((g.n + 15) / 16);
-        if (g.requests > 4 && g.rows < 4 * g.requests)
-            hipLaunchKernelGGL((adapter_join_kernel<T, 16>), dim3((blocks + 3) / 4), dim3(256), 0, st, g);
-        else
-            hipLaunchKernelGGL((adapter_join_kernel<T, 4>), dim3((blocks + 3) / 4), dim3(256), 0, st, g);
+        const auto join = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((blocks + 3) / 4), dim3(256), 0, st, g); };
+        if (g.requests > 4 && g.rows < 4 * g.requests) join(adapter_join_kernel<T, 16, false>);
+        else if (blocks <= 512) join(adapter_join_kernel<T, 4, true>);
+        else join(adapter_join_kernel<T, 4, false>);
         return hipGetLastError();
     }
     if (p.u_tiles > 0)

@@ -68,6 +68,11 @@ CASES = [
     ([0, 250, 257], [0, 1], 257, 392, 1544, 16, 2),                      # just too many rows for that
     ([0, 1000, 1001, 5000, 5100], [0, 1, 2, 0], 5131, 2056, 520, 24, 3),  # the large tiles
     ([0, 4000, 9000], [1, 0], 9000, 4104, 136, 72, 2),
+    # few rows: many column blocks of few requests, many requests of high rank, more than four adapters to 16 rows
+    ([0, 256], [1], 256, 1032, 2056, 256, 2),
+    ([0, 90, 91, 200], [0, -1, 1], 200, 2056, 1032, 72, 2),
+    (list(range(0, 257, 2)), [i % 33 - 1 for i in range(128)], 256, 264, 1544, 136, 32),
+    ([0, 2, 4, 6, 8, 10, 12, 14, 16, 40], [0, 1, 2, 3, 4, 5, 6, 7, 0], 40, 4104, 520, 32, 8),
 ]
 
 
