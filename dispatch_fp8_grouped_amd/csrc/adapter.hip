@@ -405,9 +405,11 @@ hipError_t launch_adapter(const AdapterArgs& g, const Plan& p, hipStream_t st) {
         hipLaunchKernelGGL((adapter_down_kernel<T>), dim3((uint32_t)(p.u_tiles * p.u_parts)), dim3(256), 0, st, g);
     using Wide = TileLoop<T, false, false, 128, 256, 2, 4, 3>;
     using Mid = TileLoop<T, false, false, 64, 128, 1, 4, 3>;
-    switch (pick_row_shape(g.rows, g.n, g.k, 1, 3)) {
-        case 0: return launch_up<QuadLoop<T, false, false, 256, 256, 4, 2>, Wide, T, 256, 256>(g, st);
-        case 1: return launch_up<Wide, TileLoop<T, false, false, 64, 256, 1, 8, 3>, T, 128, 256>(g, st);
+    using Square = TileLoop<T, false, false, 128, 128, 2, 4, 4>;
+    switch (pick_row_shape(g.rows, g.n, g.k, 1, kShape64 + 1)) {
+        case kShape256: return launch_up<QuadLoop<T, false, false, 256, 256, 4, 2>, Wide, T, 256, 256>(g, st);
+        case kShape128: return launch_up<Wide, TileLoop<T, false, false, 64, 256, 1, 8, 3>, T, 128, 256>(g, st);
+        case kShapeSquare: return launch_up<Square, TileLoop<T, false, false, 64, 128, 2, 4, 6>, T, 128, 128>(g, st);
         default: return launch_up<Mid, Mid, T, 64, 128>(g, st);
     }
 }

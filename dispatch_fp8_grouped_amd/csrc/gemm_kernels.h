@@ -484,25 +484,28 @@ struct KsStream {
 // Which tile shape a row product of these sizes runs with (forward and backward of the groups, the adapters'
 // shared product).  The time is estimated as `fixed` + steps * (a tile's time per step) * (rounds of tiles over the
 // CUs), with the microseconds that every shape measured: `alone` with one tile to a CU, `full` with `resident` tiles
-// on every CU.  The shapes in this order, bf16: at 32768 x 4096 x 7168 over 32 groups 1.77 ms, 2.03, 3.14, 5.5, 5.1;
-// at 512 x 512 x 512 over 4 groups 14.4, 9.8, 7.3, 6.1, 5.4, 6.1, 8.3 us; at 1024 x 7168 x 2048 over 32 groups
-// (weights streamed) 183, 175, 170, 188, 202, 240, 194 us; at 64 x 4096 x 7168, one group, 70, 52, 48, 35, 28, 19,
-// 53 us; at 1500 x 2048 x 4096 over 4 groups 80, 48, 46, 69, 82, 84, 38 us.
-// Over 44 sizes drawn from 4 to 32768 rows, 1 to 64 groups and 128 to 8192 columns, both directions, the shape picked took
-// 1.9 % longer than the best of them on average and 17 % at most.
+// on every CU.  The shapes in this order, bf16: at 21474 x 4344 x 7912 over 13 groups 1.67 ms, 2.12, 2.81, 3.1, 4.9,
+// 3.6, 5.8, 6.5; at 1500 x 2048 x 4096 over 4 groups 90, 49, 35, 47, 68, 44, 82, 85 us; at 1999 x 1000 x 2056 over 10
+// groups 45, 33, 24, 32, 39, 35, 40, 47; at 512 x 2048 x 8192 over 2 groups 148, 82, 54, 56, 57, 37, 67, 60; at 1024 x
+// 7168 x 2048 over 32 groups (weights streamed) 215, 212, 201, 188, 191, 204, 204, 240; at 6 x 696 x 2096, one group,
+// 24, 17, 13, 17, 13, 12, 10, 9.
+// Over 56 sizes drawn from 4 to 32768 rows, 1 to 64 groups and 128 to 8192 columns, both directions, the shape picked took
+// 1.5 % longer than the best of them on average and 16 % at most.
 struct RowShape {
     int bm, bn, resident;
     double fixed, alone, full;
 };
-enum { kShape256, kShape128, kShape64, kShape32, kShapeLeast, kShapeDeep, kShapeHalved };
-constexpr RowShape kRowShapes[] = {{256, 256, 1, 8.5, 1.08, 1.70},    // quadrants
+enum { kShape256, kShape128, kShapeSquare, kShape64, kShape32, kShapeHalved, kShapeLeast, kShapeDeep };
+constexpr RowShape kRowShapes[] = {{256, 256, 1, 8.5, 1.08, 1.60},    // quadrants
                                    {128, 256, 1, 5.5, 0.58, 1.02},
+                                   {128, 128, 1, 5.0, 0.34, 0.62},    // four stages: three steps for a load to arrive
                                    {64, 128, 2, 4.2, 0.40, 0.84},
-                                   {32, 128, 2, 3.8, 0.29, 0.715},
-                                   {32, 64, 2, 3.6, 0.21, 0.35},      // the ones from here on are the forward's only
-                                   {32, 64, 1, 4.8, 0.125, 0.26},     // four groups of waves along the contraction
-                                   {128, 128, 1, 5.0, 0.50, 0.62}};   // two groups
-// choices: how many of them the product has.  Groups end inside a tile, half a tile to a group on average.
+                                   {32, 128, 2, 3.8, 0.29, 0.67},
+                                   {64, 128, 1, 4.6, 0.31, 0.52},     // two groups of waves along the contraction
+                                   {32, 64, 2, 3.6, 0.17, 0.37},      // the forward's only, and the next
+                                   {32, 64, 1, 4.8, 0.125, 0.26}};    // four groups
+// choices: how many of them the product has.  Groups end inside a tile, half a tile to a group on average, or have one
+// tile each where they are short.
 inline int pick_row_shape(int rows, int cols, int depth, int groups, int choices) {
     int best = 0;
     double least = 0;
@@ -510,8 +513,9 @@ inline int pick_row_shape(int rows, int cols, int depth, int groups, int choices
     const double steps = (depth + kStepK - 1) / kStepK;
     for (int i = 0; i < choices; ++i) {
         const RowShape& s = kRowShapes[i];
-        double row_tiles = groups == 1 ? (rows + s.bm - 1) / s.bm : (double)rows / s.bm + 0.5 * used;
-        if (row_tiles < used) row_tiles = used;
+        const double row_tiles = groups == 1                       ? (rows + s.bm - 1) / s.bm
+                                 : (double)rows < 0.6 * s.bm * used ? used
+                                                                    : (double)rows / s.bm + 0.5 * used;
         const double tiles = row_tiles * ((cols + s.bn - 1) / s.bn), rounds = tiles / (256.0 * s.resident);
         // one group's tiles are counted exactly, and one more than a round holds starts another; the count of several is
         // an estimate, and their short last tiles soften the step

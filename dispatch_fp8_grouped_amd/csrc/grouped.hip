@@ -230,23 +230,25 @@ template <class T, bool B>
 hipError_t launch_rows(const GroupedArgs& a, hipStream_t st) {
     using Wide = TileLoop<T, false, B, 128, 256, 2, 4, 3>;
     using Low = TileLoop<T, false, B, 64, 256, 1, 8, 3>;
+    using Square = TileLoop<T, false, B, 128, 128, 2, 4, 4>;
     using Mid = TileLoop<T, false, B, 64, 128, 1, 4, 3>;
     using Small = TileLoop<T, false, B, 32, 128, 1, 4, 4>;
-    // a KS operand needs 128 columns, and gained nothing from groups of waves (300 x 6000 x 600: 31.6 us with and
-    // without): those shapes are the forward's only
-    const int shape = pick_row_shape(a.rows, B ? a.k : a.n, B ? a.n : a.k, a.groups, B ? kShape32 + 1 : kShapeHalved + 1);
+    // a KS operand needs 128 columns: the narrower shapes are the forward's only
+    const int shape = pick_row_shape(a.rows, B ? a.k : a.n, B ? a.n : a.k, a.groups, B ? kShapeHalved + 1 : kShapeDeep + 1);
     if (shape == kShape256)
         return launch_rows_with<QuadLoop<T, false, B, 256, 256, 4, 2>, Wide, T, B, 256, 256>(a, st);
     if (shape == kShape128) return launch_rows_with<Wide, Low, T, B, 128, 256>(a, st);
+    if (shape == kShapeSquare)
+        return launch_rows_with<Square, TileLoop<T, false, B, 64, 128, 2, 4, 6>, T, B, 128, 128>(a, st);
     if (shape == kShape64) return launch_rows_with<Mid, Mid, T, B, 64, 128>(a, st);
     if (shape == kShape32) return launch_rows_with<Small, Small, T, B, 32, 128>(a, st);
+    using Halved = TileLoop<T, false, B, 64, 128, 1, 4, 3, 2>;
+    if (shape == kShapeHalved) return launch_rows_with<Halved, Halved, T, B, 64, 128>(a, st);
     if constexpr (!B) {
         using Least = TileLoop<T, false, false, 32, 64, 1, 4, 5>;
         using Deep = TileLoop<T, false, false, 32, 64, 1, 4, 3, 4>;
-        using Halved = TileLoop<T, false, false, 128, 128, 2, 2, 2, 2>;
         if (shape == kShapeLeast) return launch_rows_with<Least, Least, T, false, 32, 64>(a, st);
-        if (shape == kShapeDeep) return launch_rows_with<Deep, Deep, T, false, 32, 64>(a, st);
-        return launch_rows_with<Halved, Halved, T, false, 128, 128>(a, st);
+        return launch_rows_with<Deep, Deep, T, false, 32, 64>(a, st);
     }
     return hipErrorInvalidValue;
 }

@@ -91,6 +91,10 @@ SHAPES = [
     ([700, 0, 520, 300], 2056, 4104),
     ([20000], 72, 64),
     ([9000, 0, 3, 4000], 136, 264),
+    # few tiles with long contractions, in either direction; square tiles with a short last one
+    ([250, 262], 2048, 8192),
+    ([250, 262], 8192, 2048),
+    ([260, 130, 0, 190, 300], 1032, 2056),
 ]
 
 
