@@ -275,19 +275,27 @@ int weight_parts(int64_t rows, int n, int k, int groups) {
     return (int)(parts < 1 ? 1 : parts);
 }
 
+// 128 x 128 tiles: with no more than one to a CU four stages, since nothing else hides a load (1400 rows, 1768 x 592:
+// 16 us against 21); with more of them two, so that two tiles share a CU (2000 rows, 4 x 1000 x 2056: 26 us against 28).
+template <class T, bool kFp32>
+hipError_t launch_small_weight(const GroupedArgs& a, hipStream_t st) {
+    if (weight_tiles(a.n, a.k, a.groups, 128) * a.parts <= 256)
+        return launch_weight_with<TileLoop<T, true, true, 128, 128, 2, 4, 4>, T, kFp32, 128, 128>(a, st);
+    return launch_weight_with<TileLoop<T, true, true, 128, 128, 2, 2, 2>, T, kFp32, 128, 128>(a, st);
+}
+
 template <class T, bool kFp32>
 hipError_t launch_weight(GroupedArgs a, void* workspace, hipStream_t st) {
     if (weight_tiles(a.n, a.k, a.groups, 256) >= kWeightLarge) {
         hipLaunchKernelGGL((grouped_weight_stream_kernel<T, kFp32>), dim3(8 * kStreams), dim3(512), 0, st, a);
         return hipGetLastError();
     }
-    using L = TileLoop<T, true, true, 128, 128, 2, 2, 2>;
-    if (a.parts == 1) return launch_weight_with<L, T, kFp32, 128, 128>(a, st);
+    if (a.parts == 1) return launch_small_weight<T, kFp32>(a, st);
     void* dw = a.out;
     const int accumulate = a.accumulate;
     a.out = workspace;
     a.accumulate = 0;
-    const hipError_t e = launch_weight_with<L, T, true, 128, 128>(a, st);
+    const hipError_t e = launch_small_weight<T, true>(a, st);
     if (e != hipSuccess) return e;
     const size_t values = (size_t)a.groups * a.n * a.k;
     const size_t blocks = (values + 1023) / 1024;
