@@ -755,10 +755,16 @@ __global__ __launch_bounds__(256) void order_place_kernel(OrderArgs a) {
     for (int64_t i = max(first, (int64_t)base) + tid; i < end; i += 256) a.order[i] = -1;
 }
 
-// Pairs per work-group of the three-launch form: a multiple of 4 waves x 64, and at most 1024 chunks.
-int64_t chunk_pairs(int64_t pairs) {
+// The three-launch form: pairs per work-group, a multiple of 4 waves x 64, and at most 1024 chunks of that many.  No
+// pairs are one empty chunk, whose launches write the offsets; the workspace is sized for the same count.
+struct Chunks {
+    int per, count;
+    uint64_t bytes(int experts) const { return (uint64_t)(count + 1) * experts * 4; }     // and the experts' totals
+};
+Chunks chunks_of(int64_t pairs) {
     const int64_t least = 4 * kPairsPerWave, by_chunks = (pairs + 1023) / 1024;
-    return ((by_chunks < least ? least : by_chunks) + 255) / 256 * 256;
+    const int64_t per = ((by_chunks < least ? least : by_chunks) + 255) / 256 * 256, count = (pairs + per - 1) / per;
+    return Chunks{(int)per, (int)(count > 0 ? count : 1)};
 }
 bool few_pairs(int64_t pairs, int experts) { return pairs <= kFewPairs && experts <= kFewExperts; }
 
@@ -895,8 +901,7 @@ int32_t mega_moe_group_workspace_bytes(int64_t pairs, int32_t num_local_experts,
     if (!bytes_out || pairs < 0) return MEGA_MOE_ERR_INVALID_ARG;
     if (pairs > MEGA_MOE_MAX_PAIRS || num_local_experts < 1 || num_local_experts > MEGA_MOE_MAX_EXPERTS)
         return MEGA_MOE_ERR_UNSUPPORTED;
-    const int64_t per = chunk_pairs(pairs);
-    *bytes_out = few_pairs(pairs, num_local_experts) ? 0 : (uint64_t)((pairs + per - 1) / per + 1) * num_local_experts * 4;
+    *bytes_out = few_pairs(pairs, num_local_experts) ? 0 : chunks_of(pairs).bytes(num_local_experts);
     return MEGA_MOE_OK;
 }
 
@@ -919,9 +924,9 @@ int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t
                            (18 * num_local_experts + 32) * sizeof(int), st, a);
         return hipGetLastError() == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
     }
-    a.per_chunk = (int)chunk_pairs(pairs);
-    a.chunks = (int)((pairs + a.per_chunk - 1) / a.per_chunk);
-    if (a.chunks == 0) a.chunks = 1;
+    const Chunks c = chunks_of(pairs);
+    a.per_chunk = c.per;
+    a.chunks = c.count;
     const dim3 chunks(a.chunks), block(256);
     hipLaunchKernelGGL(order_count_kernel, chunks, block, num_local_experts * sizeof(int), st, a);
     hipLaunchKernelGGL(order_scan_kernel, dim3((num_local_experts + 3) / 4), block, 0, st, a);

@@ -124,6 +124,17 @@ def test_ordering_refusals():
         assert lib.mega_moe_group_by_expert(*a, need, None) == mm.ERR_INVALID_ARG, i
 
 
+@pytest.mark.parametrize("experts", [513, 1000, 4096])
+def test_ordering_of_no_pairs_asks_for_the_tables_its_launches_write(experts):
+    """More than 512 experts take the three launches: counts of one chunk at least, and totals, an int32 per expert
+    in each, whether there are pairs or not."""
+    need = mm.mega_moe_group_workspace_bytes(0, experts)
+    assert need >= 2 * 4 * experts
+    assert need == mm.mega_moe_group_workspace_bytes(1, experts)
+    assert mm.lib().mega_moe_group_by_expert(None, 0, 0, experts, P, None, None, P, need - 1, None) == \
+        mm.ERR_WORKSPACE_TOO_SMALL
+
+
 def test_router_python_checks():
     x = torch.zeros(4, 16)
     for call in (lambda: mm.router_topk(x, 2), lambda: mm.router_topk(None, 2), lambda: mm.group_by_expert(x.long(), 4),
