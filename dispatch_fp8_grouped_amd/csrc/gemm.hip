@@ -140,7 +140,8 @@ __device__ __forceinline__ v4u swap_adjacent(v4u v) {
 // LDS DMA: every lane copies 16 bytes from base + off (or 4 bytes from its own address) to LDS at
 // dst + lane * size (dst and base wave-uniform, off per lane).  Inline asm: the waits for these writes are placed by hand
 // (wait_stage_barrier); the compiler, which cannot tell the three stages apart, would otherwise drain
-// every DMA in flight before each LDS read.  M0 is set in the same statement.
+// every DMA in flight before each LDS read.  M0 is set in the same statement, with the one wait state that the
+// DMA needs behind its write (the compiler puts an s_nop there in its own code, and does not look into asm).
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return (uint32_t)(uintptr_t)(lds_ptr)const_cast<void*>(p);
 }
@@ -152,28 +153,28 @@ __device__ __forceinline__ const void* sgpr_ptr(const void* ptr) {
     return (const void*)(uintptr_t)(((uint64_t)hi << 32) | lo);
 }
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, const void* dst) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :: "v"(off), "s"(base), "s"(lds_addr(dst)) : "memory", "m0");
 }
 // The same with the non-temporal hint, for data read once (the caches keep it at low priority)
 __device__ __forceinline__ void dma16_nt(const void* base, uint32_t off, const void* dst) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1 nt"
                  :: "v"(off), "s"(base), "s"(lds_addr(dst)) : "memory", "m0");
 }
 // 4 bytes per lane from a per-lane address (every lane active)
 __device__ __forceinline__ void dma4_lane(const void* src, const void* dst) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
                  :: "v"(src), "s"(lds_addr(dst)) : "memory", "m0");
 }
 // 4 bytes per active lane from base + off (base wave-uniform, off per lane) to LDS at dst + lane * 4
 __device__ __forceinline__ void dma4(const void* base, uint32_t off, const void* dst) {
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                  :: "v"(off), "s"(base), "s"(lds_addr(dst)) : "memory", "m0");
 }
 // 4 bytes per active lane with the cache policy of a device-scope atomic load (sc1), for schedule words
 // that other work-groups of the launch update
 __device__ __forceinline__ void dma4_coherent(const void* src, const void* dst) {
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off sc1"
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off sc1"
                  :: "v"(src), "s"(lds_addr(dst)) : "memory", "m0");
 }
 

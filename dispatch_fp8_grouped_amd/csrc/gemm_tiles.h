@@ -76,9 +76,10 @@ __device__ __forceinline__ u32x4 buffer_of(const void* base, uint32_t bytes) {
 }
 // 16 bytes per lane from descriptor + off to LDS at dst + lane * 16; zeros where off >= num_records.  Inline
 // asm: the waits for these writes are placed by hand (wait_vm_barrier), since the compiler, which cannot tell
-// the stages apart, would drain every DMA in flight before each LDS read.
+// the stages apart, would drain every DMA in flight before each LDS read.  An LDS DMA reads M0 no sooner than one wait
+// state after its write; the compiler puts the s_nop between its own, and does not look into asm.
 __device__ __forceinline__ void dma_rows(u32x4 desc, uint32_t off, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
                  :: "v"(off), "s"(desc), "s"(__builtin_amdgcn_readfirstlane(dst)) : "memory", "m0");
 }
 // At most N of this wave's vector-memory operations still outstanding and its LDS reads returned; then barrier.
