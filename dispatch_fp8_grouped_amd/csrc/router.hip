@@ -321,7 +321,8 @@ router_kernel(RouterArgs a) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = lane * EPL + j;
-            double rank = x[j], worth = x[j];
+            // clipped as in the expert's key: a group of +inf ties with one of the largest number
+            double rank = x[j], worth = kWide ? x[j] : clip_inf(x[j]);
             if (by_score && live[j]) {
                 const double s = kSigmoid ? sigmoid64(x[j]) : exp((double)clip_inf(x[j]) - (double)top) / total;
                 worth = s;
