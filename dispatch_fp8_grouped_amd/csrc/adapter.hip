@@ -15,7 +15,9 @@
 //
 // v enters the MFMA as two 16-bit numbers, hi = v rounded and lo = (v - hi) rounded: hi alone would add an
 // error of half a step of the 16-bit type to every v; the second number takes it to 2^-16 (bf16) for twice the
-// (few) operations of the second product.
+// (few) operations of the second product.  fp16 has neither room for a large v nor bits for a small one: there the 32
+// values of a row that one MFMA takes are multiplied by a power of two that brings the largest into 2^14 .. 2^15, and
+// their fp32 sum by its inverse before it joins the others.
 //
 // Measured, bf16.  64 requests of one row, rank 16, 4096 x 7168: 22 us for 68 MB (parts 16, join 7): bound by the
 // weights' stream, which has 16 us to ramp up and drain, and the latency of two launches.  8192 rows of 12 requests,
@@ -155,10 +157,19 @@ __device__ __forceinline__ i32x4 row_chunk(const uint16_t* row, int c, int cols)
     return c < cols ? *reinterpret_cast<const i32x4*>(row + c) : i32x4{0, 0, 0, 0};
 }
 
-// scale * u[m][c .. c+7] (the parts added in their order) as hi and lo; zeros from column `rank` on.  kTogether: the
+// The largest of v over the four lanes that hold a row's 32 values (l, l + 16, l + 32, l + 48); NaN does not count.
+__device__ __forceinline__ float row_largest(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// scale * u[m][c .. c+7] (the parts added in their order) as hi and lo; zeros from column `rank` on.  Returns the factor
+// of the product's sums (1 unless T::kNarrow).  All lanes take part.  kTogether: the
 // loads of up to kMostParts parts go out before the first is needed (parts that do not exist repeat the last).
 template <class T, bool kTogether>
-__device__ __forceinline__ void low_rank_row(const AdapterArgs& g, int m, int c, float scale, i32x4& hi, i32x4& lo) {
+__device__ __forceinline__ float low_rank_row(const AdapterArgs& g, int m, int c, float scale, i32x4& hi, i32x4& lo) {
     f32x4 v[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     if (c < g.rank) {
         const float* u = g.u + (size_t)m * g.rank + c;
@@ -183,11 +194,26 @@ __device__ __forceinline__ void low_rank_row(const AdapterArgs& g, int m, int c,
             }
         }
     }
+    v[0] *= scale;
+    v[1] *= scale;
+    float back = 1.f;
+    if constexpr (T::kNarrow) {
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i / 4][i % 4]));
+        // biased exponent; the factors 2^(141 - e) and 2^(e - 141) are both normal numbers for it.  Of an infinite value
+        // the factor is the largest number's, and of values below 2^-97 that of 2^-97
+        const uint32_t e = min(max(__float_as_uint(row_largest(most)) >> 23, 30u), 254u);
+        const float up = __uint_as_float((268 - e) << 23);
+        back = __uint_as_float((e - 14) << 23);
+        v[0] *= up;
+        v[1] *= up;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const float a = v[h][2 * p] * scale, b = v[h][2 * p + 1] * scale;
+            const float a = v[h][2 * p], b = v[h][2 * p + 1];
             const uint32_t w = T::pack(a, b);
             float ra = a - T::low(w), rb = b - T::high(w);
             ra = fabsf(ra) < __builtin_inff() ? ra : 0.f;          // hi alone carries inf and NaN
@@ -195,6 +221,14 @@ __device__ __forceinline__ void low_rank_row(const AdapterArgs& g, int m, int c,
             hi[h * 2 + p] = (int)w;
             lo[h * 2 + p] = (int)T::pack(ra, rb);
         }
+    return back;
+}
+
+// sum + q (hi + lo), `back` from low_rank_row
+template <class T>
+__device__ __forceinline__ f32x4 add_low_rank(i32x4 q, i32x4 hi, i32x4 lo, float back, f32x4 sum) {
+    if constexpr (T::kNarrow) return sum + back * T::mfma(q, lo, T::mfma(q, hi, f32x4{0.f, 0.f, 0.f, 0.f}));
+    else return T::mfma(q, lo, T::mfma(q, hi, sum));
 }
 
 // Few rows: a wave per 16 x 16 block of y adds up the parts and its rows' adapters.  It is bound by the latency of its
@@ -235,12 +269,9 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(AdapterArgs g) {
             for (int i = 0; i < kAtOnce; ++i)
                 q[i] = row_chunk(g.b + ((size_t)max(id[i], 0) * g.n + nq) * g.rank, c, id[i] >= 0 ? g.rank : 0);
             // a row without an adapter has no u: its lanes stay at zero
-            low_rank_row<T, kTogether>(g, m, ad >= 0 ? c : g.rank, scale, hi, lo);
+            const float back = low_rank_row<T, kTogether>(g, m, ad >= 0 ? c : g.rank, scale, hi, lo);
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                delta[i] = T::mfma(q[i], hi, delta[i]);
-                delta[i] = T::mfma(q[i], lo, delta[i]);
-            }
+            for (int i = 0; i < kAtOnce; ++i) delta[i] = add_low_rank<T>(q[i], hi, lo, back, delta[i]);
         }
         // only its own rows: another request's infinity must not reach a row by way of 0 * inf
 #pragma unroll
@@ -301,10 +332,10 @@ __device__ __forceinline__ void up_tile(const AdapterArgs& g, int m0, int q0, ui
                 // not reach a row by way of 0 * inf
                 const bool mine = m >= lo && m < lo + cnt;
                 i32x4 hi, lo16;
-                low_rank_row<T, false>(g, min(m, g.rows - 1), mine ? c : g.rank, scale, hi, lo16);
+                const float back = low_rank_row<T, false>(g, min(m, g.rows - 1), mine ? c : g.rank, scale, hi, lo16);
 #pragma unroll
                 for (int i = 0; i < L::QI; ++i) {
-                    const f32x4 sum = T::mfma(q[i], lo16, T::mfma(q[i], hi, acc[i][j]));
+                    const f32x4 sum = add_low_rank<T>(q[i], hi, lo16, back, acc[i][j]);
                     acc[i][j] = mine ? sum : acc[i][j];
                 }
             }

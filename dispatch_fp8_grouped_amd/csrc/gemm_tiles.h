@@ -34,8 +34,10 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void* lds_void;
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
-// Element types: the MFMA, and rounding (to nearest even) of two fp32 values into one word.
+// Element types: the MFMA, and rounding (to nearest even) of two fp32 values into one word; kNarrow: fewer exponents
+// than fp32.
 struct Bf16 {
+    static constexpr bool kNarrow = false;
     static __device__ __forceinline__ f32x4 mfma(i32x4 a, i32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
                                                        0, 0, 0);
@@ -47,6 +49,7 @@ struct Bf16 {
     static __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 };
 struct Fp16 {
+    static constexpr bool kNarrow = true;
     static __device__ __forceinline__ f32x4 mfma(i32x4 a, i32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                       0, 0);

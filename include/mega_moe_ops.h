@@ -145,8 +145,9 @@ int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t
  *   requests 0 .. MEGA_MOE_MAX_REQUESTS; adapters 1 .. 65536; rows, n, k, dtype as above
  *   workspace mega_moe_adapter_workspace_bytes() bytes; its contents do not matter
  * The shared sum, x a^T and the adapter's sum are held in fp32; scales[a] * x a^T enters the second product as
- * the sum of two 16-bit numbers, the value rounded and the rounded remainder.  In fp16 it has fp16's range:
- * beyond 65504 it is infinite, below 6e-8 it is 0.
+ * the sum of two 16-bit numbers, the value rounded and the rounded remainder: an error of 2^-16 of it in bf16 and 2^-22
+ * in fp16, where a power of two per row and 32 ranks gives it fp32's range (and values below 2^-39 of the largest of
+ * their 32 count as 0).
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP. */
 int32_t mega_moe_adapter_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t rank, int32_t requests,
                                          uint64_t* bytes_out /* host */);
