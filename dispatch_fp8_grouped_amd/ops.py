@@ -12,8 +12,10 @@ devices, allocate what they return, and call them.  Everything runs in the HIP k
     y = mm.adapter_forward(x, w, a, b, scales, offsets, adapter)     # one low-rank adapter per request
 
 Tensors must be dense, on one GPU.  Calls run on the current stream of that GPU, or on `stream` (a torch
-stream or a stream handle); a tensor that a call returns belongs to the stream of the call.  The functions
-compute values and gradients and record no autograd graph.
+stream or a stream handle); a tensor that a call returns belongs to the stream of the call.  The tensors given
+with `stream` are recorded on it, so that their memory is not handed out again before the call has read it; that
+they are ready by then is up to the caller, as for any stream.  The functions compute values and gradients and
+record no autograd graph.
 """
 from __future__ import annotations
 
@@ -160,10 +162,10 @@ def _want(name, t, shape, dtypes, device=None):
 
 
 class _Call:
-    """Makes `device` and the call's stream current, so that allocations belong to that stream; `raw` is the
-    stream's handle."""
+    """Makes `device` and the call's stream current, so that allocations belong to that stream, and records the
+    call's tensors on a stream that was given; `raw` is the stream's handle."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, *tensors):
         import torch
         self.ctx = None
         if stream is None:
@@ -177,6 +179,9 @@ class _Call:
                 stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
             if stream.device != device:
                 raise ValueError(f"stream of {stream.device} for tensors on {device}")
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
             self.ctx = torch.cuda.stream(stream)
             self.raw = stream.cuda_stream
 
@@ -219,7 +224,7 @@ def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream):
         _want("status", status, (1,), (torch.int32,), w.device)
     lib = _mm.lib()
     call = lib.mega_moe_grouped_forward if contract_k else lib.mega_moe_grouped_backward_rows
-    with _Call(w.device, stream) as raw:
+    with _Call(w.device, stream, rows_in, w, offsets, out, status) as raw:
         if out is None:
             out = torch.empty((rows, outer), dtype=w.dtype, device=w.device)
         else:
@@ -264,7 +269,7 @@ def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=Fal
     if status is not None:
         _want("status", status, (1,), (torch.int32,), x.device)
     nbytes = _weight_bytes(rows, n, k, groups)
-    with _Call(x.device, stream) as raw:
+    with _Call(x.device, stream, dy, x, offsets, out, status) as raw:
         if out is None:
             out = torch.empty((groups, n, k), dtype=dtype, device=x.device)
         else:
@@ -306,7 +311,7 @@ def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_gro
     if bias is not None:
         _want("bias", bias, (cfg.num_experts,), (torch.float32,), logits.device)
     shape = (*logits.shape[:-1], max(topk, 0))
-    with _Call(logits.device, stream) as raw:
+    with _Call(logits.device, stream, logits, bias) as raw:
         idx = torch.empty(shape, dtype=torch.int64, device=logits.device)
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
         _mm._check(_mm.lib().mega_moe_router_topk(cfg, logits.data_ptr(), _at(bias), idx.data_ptr(), weights.data_ptr(),
@@ -323,7 +328,7 @@ def router_backward(dweights, logits, topk_idx, score="softmax", renormalize=Tru
     cfg = _router_config(logits, topk, score, 1, 1, 1, renormalize, scale)
     _want("topk_idx", topk_idx, (*logits.shape[:-1], topk), (torch.int64,), logits.device)
     _want("dweights", dweights, (*logits.shape[:-1], topk), (torch.float32,), logits.device)
-    with _Call(logits.device, stream) as raw:
+    with _Call(logits.device, stream, dweights, logits, topk_idx) as raw:
         dlogits = torch.empty_like(logits)
         _mm._check(_mm.lib().mega_moe_router_backward(cfg, dweights.data_ptr(), logits.data_ptr(), topk_idx.data_ptr(),
                                                       dlogits.data_ptr(), raw), "router_backward")
@@ -338,7 +343,7 @@ def group_by_expert(topk_idx, num_local_experts, first_expert=0, stream=None):
     _want("topk_idx", topk_idx, None, (torch.int64,))
     pairs, device = topk_idx.numel(), topk_idx.device
     nbytes = _group_bytes(pairs, num_local_experts)
-    with _Call(device, stream) as raw:
+    with _Call(device, stream, topk_idx) as raw:
         offsets = torch.empty(num_local_experts + 1, dtype=torch.int32, device=device)
         order = torch.empty(pairs, dtype=torch.int32, device=device)
         slot = torch.empty(topk_idx.shape, dtype=torch.int32, device=device)
@@ -372,7 +377,7 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
     if status is not None:
         _want("status", status, (1,), (torch.int32,), w.device)
     nbytes = _adapter_bytes(rows, n, k, rank, requests)
-    with _Call(w.device, stream) as raw:
+    with _Call(w.device, stream, x, w, a, b, scales, offsets, adapter, out, workspace, status) as raw:
         if out is None:
             out = torch.empty((rows, n), dtype=w.dtype, device=w.device)
         else:

@@ -1,0 +1,80 @@
+"""How the operators' Python calls treat the tensors and streams of their caller."""
+import pytest
+import torch
+
+import dispatch_fp8_grouped_amd as mm
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def case(rows=300, n=264, k=136, groups=3, seed=0):
+    """Arguments of every operator, made anew."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*shape, dtype=BF16):
+        return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+    off = torch.tensor([rows * i // groups for i in range(groups + 1)], dtype=torch.int32, device="cuda")
+    idx = torch.randint(0, 32, (rows, 4), generator=g, device="cuda")
+    return {
+        "grouped_forward": lambda: dict(x=normal(rows, k), w=normal(groups, n, k), offsets=off.clone()),
+        "grouped_backward_rows": lambda: dict(dy=normal(rows, n), w=normal(groups, n, k), offsets=off.clone()),
+        "grouped_backward_weight": lambda: dict(dy=normal(rows, n), x=normal(rows, k), offsets=off.clone()),
+        "router_topk": lambda: dict(logits=normal(rows, 32, dtype=torch.float32), topk=4,
+                                    bias=normal(32, dtype=torch.float32)),
+        "router_backward": lambda: dict(dweights=normal(rows, 4, dtype=torch.float32),
+                                        logits=normal(rows, 32, dtype=torch.float32), topk_idx=idx.clone()),
+        "group_by_expert": lambda: dict(topk_idx=idx.clone(), num_local_experts=32),
+        "adapter_forward": lambda: dict(x=normal(rows, k), w=normal(n, k), a=normal(2, 16, k), b=normal(2, n, 16),
+                                        scales=normal(2, dtype=torch.float32), offsets=off.clone(),
+                                        adapter=torch.tensor([0, 1, -1], dtype=torch.int32, device="cuda")),
+    }
+
+
+OPERATORS = list(case())
+
+
+def outputs(y):
+    return list(y) if isinstance(y, tuple) else [y]
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_tensors_dropped_after_a_call_on_another_stream_stay_until_it_has_read_them(name):
+    """The call waits behind other work of its stream while its inputs are dropped and their sizes asked for again."""
+    call, side = getattr(mm, name), torch.cuda.Stream()
+    want = [t.clone() for t in outputs(call(**case()[name]()))]
+    args = case()[name]()
+    tensors = {k: v for k, v in args.items() if isinstance(v, torch.Tensor)}
+    sizes = [(v.shape, v.dtype) for v in tensors.values()]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    got = outputs(call(**args, stream=side))
+    del args, tensors
+    again = [torch.zeros(s, dtype=d, device="cuda") for s, d in sizes for _ in range(4)]
+    side.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    del again
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_a_captured_call_with_its_stream_given(name):
+    call, args = getattr(mm, name), case()[name]()
+    want = [t.clone() for t in outputs(call(**args))]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = outputs(call(**args, stream=torch.cuda.current_stream()))
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+    del args                                           # recorded on the capture's stream
+    more = torch.zeros(1 << 20, device="cuda")
+    torch.cuda.synchronize()
+    del more, graph
