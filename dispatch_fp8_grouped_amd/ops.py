@@ -11,7 +11,8 @@ devices, allocate what they return, and call them.  Everything runs in the HIP k
     dw = mm.grouped_backward_weight(dy, x_sorted, offsets)
     y = mm.adapter_forward(x, w, a, b, scales, offsets, adapter)     # one low-rank adapter per request
 
-Tensors must be dense, on one GPU.  Calls run on the current stream of that GPU, or on `stream` (a torch
+Tensors must be dense, on one GPU; a slice of tokens that the router or the ordering is given may start anywhere,
+and the other tensors start at a multiple of 16 bytes, as slices of their rows do.  Calls run on the current stream of that GPU, or on `stream` (a torch
 stream or a stream handle); a tensor that a call returns belongs to the stream of the call.  The tensors given
 with `stream` are recorded on it, so that their memory is not handed out again before the call has read it; that
 they are ready by then is up to the caller, as for any stream.  The functions compute values and gradients and
@@ -209,6 +210,12 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _from16(t):
+    """t, or a copy of it where it does not start at a multiple of 16 bytes, which the library asks for: a slice of
+    tokens whose rows are no such multiple (bfloat16 logits of 60 experts, ids of an odd topk)."""
+    return t if t is None or not t.data_ptr() & 15 else t.clone()
+
+
 def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream):
     import torch
     kinds = _halves()
@@ -312,6 +319,7 @@ def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_gro
         _want("bias", bias, (cfg.num_experts,), (torch.float32,), logits.device)
     shape = (*logits.shape[:-1], max(topk, 0))
     with _Call(logits.device, stream, logits, bias) as raw:
+        logits, bias = _from16(logits), _from16(bias)
         idx = torch.empty(shape, dtype=torch.int64, device=logits.device)
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
         _mm._check(_mm.lib().mega_moe_router_topk(cfg, logits.data_ptr(), _at(bias), idx.data_ptr(), weights.data_ptr(),
@@ -329,6 +337,7 @@ def router_backward(dweights, logits, topk_idx, score="softmax", renormalize=Tru
     _want("topk_idx", topk_idx, (*logits.shape[:-1], topk), (torch.int64,), logits.device)
     _want("dweights", dweights, (*logits.shape[:-1], topk), (torch.float32,), logits.device)
     with _Call(logits.device, stream, dweights, logits, topk_idx) as raw:
+        dweights, logits, topk_idx = _from16(dweights), _from16(logits), _from16(topk_idx)
         dlogits = torch.empty_like(logits)
         _mm._check(_mm.lib().mega_moe_router_backward(cfg, dweights.data_ptr(), logits.data_ptr(), topk_idx.data_ptr(),
                                                       dlogits.data_ptr(), raw), "router_backward")
@@ -344,6 +353,7 @@ def group_by_expert(topk_idx, num_local_experts, first_expert=0, stream=None):
     pairs, device = topk_idx.numel(), topk_idx.device
     nbytes = _group_bytes(pairs, num_local_experts)
     with _Call(device, stream, topk_idx) as raw:
+        topk_idx = _from16(topk_idx)
         offsets = torch.empty(num_local_experts + 1, dtype=torch.int32, device=device)
         order = torch.empty(pairs, dtype=torch.int32, device=device)
         slot = torch.empty(topk_idx.shape, dtype=torch.int32, device=device)

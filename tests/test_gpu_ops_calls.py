@@ -78,3 +78,28 @@ def test_a_captured_call_with_its_stream_given(name):
     more = torch.zeros(1 << 20, device="cuda")
     torch.cuda.synchronize()
     del more, graph
+
+
+@pytest.mark.parametrize("kind", [torch.float32, BF16, torch.float16])
+@pytest.mark.parametrize("experts,topk", [(60, 3), (7, 5), (256, 8), (1001, 1)])
+def test_slices_of_tokens_that_start_anywhere(experts, topk, kind):
+    """Slices whose rows are no multiple of 16 bytes, bias and ids from the middle of a tensor."""
+    g = torch.Generator(device="cuda").manual_seed(experts)
+    logits = torch.randn(40, experts, generator=g, device="cuda").to(kind)
+    bias = torch.randn(experts + 1, generator=g, device="cuda")[1:]
+    dweights = torch.randn(40, topk, generator=g, device="cuda")
+    side = torch.cuda.Stream()
+    for score in ("softmax", "sigmoid"):
+        whole = mm.router_topk(logits, topk, bias=bias.clone(), score=score)
+        grads = mm.router_backward(dweights, logits, whole[0], score=score)
+        torch.cuda.synchronize()
+        for lo, hi, stream in ((1, 40, None), (3, 17, side), (39, 40, None), (40, 40, None)):
+            idx, weights = mm.router_topk(logits[lo:hi], topk, bias=bias, score=score, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(idx, whole[0][lo:hi]) and torch.equal(weights, whole[1][lo:hi])
+            d = mm.router_backward(dweights[lo:hi], logits[lo:hi], whole[0][lo:hi], score=score, stream=stream)
+            some = mm.group_by_expert(whole[0][lo:hi], experts, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(d, grads[lo:hi])
+            for a, b in zip(some, mm.group_by_expert(whole[0][lo:hi].clone(), experts)):
+                assert torch.equal(a, b)
