@@ -12,11 +12,15 @@ devices, allocate what they return, and call them.  Everything runs in the HIP k
     y = mm.adapter_forward(x, w, a, b, scales, offsets, adapter)     # one low-rank adapter per request
 
 Tensors must be dense, on one GPU; a slice of tokens that the router or the ordering is given may start anywhere,
-and the other tensors start at a multiple of 16 bytes, as slices of their rows do.  Calls run on the current stream of that GPU, or on `stream` (a torch
-stream or a stream handle); a tensor that a call returns belongs to the stream of the call.  The tensors given
-with `stream` are recorded on it, so that their memory is not handed out again before the call has read it; that
-they are ready by then is up to the caller, as for any stream.  The functions compute values and gradients and
-record no autograd graph.
+and the other tensors start at a multiple of 16 bytes, as slices of their rows do.  Calls run on the current
+stream of that GPU, or on `stream` (a torch stream or a stream handle); a tensor that a call returns belongs to the
+stream of the call.  The tensors given with `stream` are recorded on it, so that their memory is not handed out
+again before the call has read it; that they are ready by then is up to the caller, as for any stream.
+
+The functions compute values and gradients; autograd does not derive the one from the other.  Where it records and
+an input requires a gradient, what grouped_forward, router_topk (its weights) and adapter_forward return carries a node
+that raises in backward(), so that no parameter goes without its gradient unnoticed; what the gradient calls return,
+and what is written into `out`, is recorded nowhere.
 """
 from __future__ import annotations
 
@@ -162,20 +166,28 @@ def _want(name, t, shape, dtypes, device=None):
                      f"{'' if device is None else ' on ' + str(device)}, got {got}")
 
 
+@functools.lru_cache(None)
+def _current():
+    import torch
+    return torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 class _Call:
     """Makes `device` and the call's stream current, so that allocations belong to that stream, and records the
     call's tensors on a stream that was given; `raw` is the stream's handle."""
 
     def __init__(self, device, stream, *tensors):
-        import torch
         self.ctx = None
         if stream is None:
-            if torch._C._cuda_getDevice() != device.index:
-                self.ctx = torch.cuda.device(device)
             # the handle of torch.cuda.current_stream(device), without making the object: the host time
             # of a call went from 12.4 to 8.6 us with it, and small calls are bound by that
-            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
+            current_device, current_stream = _current()
+            if current_device() != device.index:
+                import torch
+                self.ctx = torch.cuda.device(device)
+            self.raw = current_stream(device.index)
         else:
+            import torch
             if isinstance(stream, int):
                 stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
             if stream.device != device:
@@ -206,8 +218,39 @@ def _halves():
     return _KINDS
 
 
+@functools.lru_cache(None)
+def _logit_kinds():
+    import torch
+    return {**_halves(), torch.float32: FP32}
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(None)
+def _stop():
+    import torch
+
+    class NoGraph(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, what, how, out, *inputs):
+            ctx.message = f"{what} records no autograd graph: {how}, or call it under torch.no_grad()"
+            return out.detach()
+
+        @staticmethod
+        def backward(ctx, *grads):
+            raise RuntimeError(ctx.message)
+    return NoGraph.apply
+
+
+def _unrecorded(what, how, out, *inputs):
+    """`out`, with a node that raises where autograd would pass through it to inputs that require a gradient."""
+    for t in inputs:
+        if t.requires_grad:
+            import torch
+            return _stop()(what, how, out, *inputs) if torch.is_grad_enabled() else out
+    return out
 
 
 def _from16(t):
@@ -247,7 +290,9 @@ def grouped_forward(x, w, offsets, out=None, status=None, stream=None):
     x [rows, k], w [groups, n, k], both bfloat16 or float16; offsets int32 [groups + 1].  Rows that belong
     to no group are not written (in a new `out` they hold what the allocation held).  status: int32 [1], or
     None; see mega_moe_ops.h."""
-    return _grouped("grouped_forward", x, w, offsets, True, out, status, stream)
+    y = _grouped("grouped_forward", x, w, offsets, True, out, status, stream)
+    return y if out is not None else _unrecorded(
+        "grouped_forward", "compute its gradients with grouped_backward_rows and grouped_backward_weight", y, x, w)
 
 
 def grouped_backward_rows(dy, w, offsets, out=None, status=None, stream=None):
@@ -293,16 +338,15 @@ _config = functools.lru_cache(1024)(mega_moe_router_config)
 
 
 def _router_config(logits, topk, score, num_groups, topk_groups, group_top, renormalize, scale):
-    import torch
-    _want("logits", logits, None, (torch.float32, *_halves()))
+    kinds = _logit_kinds()
+    _want("logits", logits, None, kinds)
     if logits.dim() < 2 or logits.shape[-1] < 1:
         raise ValueError(f"logits: want [..., num_experts], got {tuple(logits.shape)}")
     if score not in _SCORES:
         raise ValueError(f"score: want one of {sorted(_SCORES)}, got {score!r}")
     experts = logits.shape[-1]
-    kind = FP32 if logits.dtype == torch.float32 else _halves()[logits.dtype]
     return _config(logits.numel() // experts, experts, topk, _SCORES[score], num_groups, topk_groups, group_top,
-                   1 if renormalize else 0, scale, kind)
+                   1 if renormalize else 0, scale, kinds[logits.dtype])
 
 
 def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_groups=1, group_top=1, renormalize=True,
@@ -314,6 +358,7 @@ def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_gro
     [num_experts], added to the scores for the choice only.  Only experts of the topk_groups best of num_groups
     equal groups are eligible; a group is worth the sum of its group_top (1 or 2) best.  See mega_moe_ops.h."""
     import torch
+    given = logits
     cfg = _router_config(logits, topk, score, num_groups, topk_groups, group_top, renormalize, scale)
     if bias is not None:
         _want("bias", bias, (cfg.num_experts,), (torch.float32,), logits.device)
@@ -324,7 +369,7 @@ def router_topk(logits, topk, bias=None, score="softmax", num_groups=1, topk_gro
         weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
         _mm._check(_mm.lib().mega_moe_router_topk(cfg, logits.data_ptr(), _at(bias), idx.data_ptr(), weights.data_ptr(),
                                                   raw), "router_topk")
-    return idx, weights
+    return idx, _unrecorded("router_topk", "compute the gradient of its weights with router_backward", weights, given)
 
 
 def router_backward(dweights, logits, topk_idx, score="softmax", renormalize=True, scale=1.0, stream=None):
@@ -387,6 +432,7 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
     if status is not None:
         _want("status", status, (1,), (torch.int32,), w.device)
     nbytes = _adapter_bytes(rows, n, k, rank, requests)
+    fresh = out is None
     with _Call(w.device, stream, x, w, a, b, scales, offsets, adapter, out, workspace, status) as raw:
         if out is None:
             out = torch.empty((rows, n), dtype=w.dtype, device=w.device)
@@ -400,4 +446,4 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
             x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), offsets.data_ptr(), adapter.data_ptr(),
             out.data_ptr(), rows, n, k, rank, requests, adapters, kinds[w.dtype], workspace.data_ptr(), workspace.numel(),
             _at(status), raw), "adapter_forward")
-    return out
+    return _unrecorded("adapter_forward", "it serves adapters and has no gradient", out, x, w, a, b, scales) if fresh else out

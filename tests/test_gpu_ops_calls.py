@@ -103,3 +103,32 @@ def test_slices_of_tokens_that_start_anywhere(experts, topk, kind):
             assert torch.equal(d, grads[lo:hi])
             for a, b in zip(some, mm.group_by_expert(whole[0][lo:hi].clone(), experts)):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name,inputs", [("grouped_forward", ("x", "w")), ("router_topk", ("logits",)),
+                                         ("adapter_forward", ("x", "w", "a", "b", "scales"))])
+def test_a_gradient_is_not_lost_silently(name, inputs):
+    call, args = getattr(mm, name), case()[name]()
+    want = outputs(call(**args))
+    for key in inputs:
+        with_grad = {**args, key: args[key].clone().requires_grad_()}
+        got = outputs(call(**with_grad))
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+            assert b.requires_grad == b.is_floating_point()
+        with pytest.raises(RuntimeError, match=f"{name} records no autograd graph"):
+            got[-1].float().sum().backward()
+        with torch.no_grad():
+            assert not any(t.requires_grad for t in outputs(call(**with_grad)))
+        if name != "router_topk":                      # into a buffer of the caller's: as it was
+            out = torch.empty_like(want[0])
+            assert call(**with_grad, out=out) is out and not out.requires_grad
+
+
+@pytest.mark.parametrize("name,inputs", [("grouped_backward_rows", ("dy", "w")), ("grouped_backward_weight", ("dy", "x")),
+                                         ("router_backward", ("dweights", "logits"))])
+def test_gradients_are_plain_tensors(name, inputs):
+    args = case()[name]()
+    for key in inputs:
+        args[key].requires_grad_()
+    assert not getattr(mm, name)(**args).requires_grad

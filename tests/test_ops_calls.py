@@ -1,0 +1,32 @@
+"""What the operators' Python calls do with their caller's tensors before and after the library, without a GPU."""
+import pytest
+import torch
+
+from dispatch_fp8_grouped_amd import ops
+
+
+def test_a_result_raises_where_a_gradient_would_be_lost():
+    x, w = torch.randn(3, 4, requires_grad=True), torch.randn(4)
+    y = ops._unrecorded("op", "do so", torch.zeros(3, 4), w, x)
+    assert y.requires_grad and (y == 0).all()
+    y.mul_(2)                                          # an ordinary tensor otherwise
+    with pytest.raises(RuntimeError, match="op records no autograd graph: do so"):
+        (y * x).sum().backward()
+
+
+def test_a_result_is_left_alone_where_no_gradient_is_asked_for():
+    out, x, p = torch.zeros(3), torch.randn(3), torch.randn(3, requires_grad=True)
+    assert ops._unrecorded("op", "", out, x) is out
+    with torch.no_grad():
+        assert ops._unrecorded("op", "", out, p) is out
+
+    class Own(torch.autograd.Function):                # a program's own node around the calls
+        @staticmethod
+        def forward(ctx, a):
+            return ops._unrecorded("op", "", a * 2, a)
+
+        @staticmethod
+        def backward(ctx, g):
+            return 2 * g
+    Own.apply(p).sum().backward()
+    assert (p.grad == 2).all()
