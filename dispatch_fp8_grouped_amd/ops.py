@@ -148,10 +148,30 @@ def mega_moe_adapter_forward(x, w, a, b, scales, offsets, adapter, y, rows, n, k
 
 
 # --------------------------------------------------------------- checks
+def _int32(**sizes):
+    """Each of them fits the library's int32: ctypes would pass its low 32 bits without a word."""
+    for name, v in sizes.items():
+        if not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{name}: want a 32-bit integer, got {v}")
+
+
 # Sizes ask for the same workspace every time; the queries' ctypes calls would be a fifth of a small call's host time.
-_weight_bytes = functools.lru_cache(1024)(mega_moe_grouped_weight_workspace_bytes)
-_group_bytes = functools.lru_cache(1024)(mega_moe_group_workspace_bytes)
-_adapter_bytes = functools.lru_cache(1024)(mega_moe_adapter_workspace_bytes)
+@functools.lru_cache(1024)
+def _weight_bytes(rows, n, k, groups):
+    _int32(n=n, k=k, groups=groups)
+    return mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups)
+
+
+@functools.lru_cache(1024)
+def _group_bytes(pairs, num_local_experts):
+    _int32(num_local_experts=num_local_experts)
+    return mega_moe_group_workspace_bytes(pairs, num_local_experts)
+
+
+@functools.lru_cache(1024)
+def _adapter_bytes(rows, n, k, rank, requests, adapters):
+    _int32(n=n, k=k, rank=rank, requests=requests, adapters=adapters)
+    return mega_moe_adapter_workspace_bytes(rows, n, k, rank, requests)
 
 
 def _want(name, t, shape, dtypes, device=None):
@@ -266,6 +286,8 @@ def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream):
     if w.dim() != 3 or rows_in is None or rows_in.dim() != 2:
         raise ValueError(f"{what}: want w [groups, n, k] and rows of two dimensions")
     groups, n, k = w.shape
+    if (groups | n | k) >> 31:
+        _int32(groups=groups, n=n, k=k)
     inner, outer = (k, n) if contract_k else (n, k)
     rows = rows_in.shape[0]
     _want("x" if contract_k else "dy", rows_in, (rows, inner), (w.dtype,), w.device)
@@ -334,7 +356,11 @@ def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=Fal
     return out
 
 
-_config = functools.lru_cache(1024)(mega_moe_router_config)
+@functools.lru_cache(1024)
+def _config(tokens, num_experts, topk, score, num_groups, topk_groups, group_top, renormalize, scale, dtype):
+    _int32(num_experts=num_experts, topk=topk, num_groups=num_groups, topk_groups=topk_groups, group_top=group_top)
+    return mega_moe_router_config(tokens, num_experts, topk, score, num_groups, topk_groups, group_top, renormalize,
+                                  scale, dtype)
 
 
 def _router_config(logits, topk, score, num_groups, topk_groups, group_top, renormalize, scale):
@@ -397,6 +423,8 @@ def group_by_expert(topk_idx, num_local_experts, first_expert=0, stream=None):
     _want("topk_idx", topk_idx, None, (torch.int64,))
     pairs, device = topk_idx.numel(), topk_idx.device
     nbytes = _group_bytes(pairs, num_local_experts)
+    if first_expert >> 31:
+        _int32(first_expert=first_expert)
     with _Call(device, stream, topk_idx) as raw:
         topk_idx = _from16(topk_idx)
         offsets = torch.empty(num_local_experts + 1, dtype=torch.int32, device=device)
@@ -431,7 +459,7 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
     _want("adapter", adapter, (requests,), (torch.int32,), device)
     if status is not None:
         _want("status", status, (1,), (torch.int32,), w.device)
-    nbytes = _adapter_bytes(rows, n, k, rank, requests)
+    nbytes = _adapter_bytes(rows, n, k, rank, requests, adapters)
     fresh = out is None
     with _Call(w.device, stream, x, w, a, b, scales, offsets, adapter, out, workspace, status) as raw:
         if out is None:

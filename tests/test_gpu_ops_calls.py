@@ -132,3 +132,20 @@ def test_gradients_are_plain_tensors(name, inputs):
     for key in inputs:
         args[key].requires_grad_()
     assert not getattr(mm, name)(**args).requires_grad
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    logits = torch.randn(3, 32, device="cuda")
+    idx = torch.randint(0, 32, (3, 4), device="cuda")
+    wide = torch.empty(0, (1 << 32) + 16, dtype=BF16, device="cuda")
+    off = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for call in (lambda: mm.router_topk(logits, (1 << 32) + 2), lambda: mm.router_topk(logits, 2, num_groups=(1 << 32) + 2),
+                 lambda: mm.router_topk(logits, 2, num_groups=2, topk_groups=(1 << 32) + 1),
+                 lambda: mm.router_topk(logits, 2, num_groups=2, group_top=(1 << 32) + 1),
+                 lambda: mm.group_by_expert(idx, (1 << 32) + 8), lambda: mm.group_by_expert(idx, 8, first_expert=1 << 32),
+                 lambda: mm.group_by_expert(idx, 8, first_expert=-(1 << 32)),
+                 lambda: mm.grouped_backward_weight(torch.empty(0, 8, dtype=BF16, device="cuda"), wide, off)):
+        with pytest.raises(ValueError, match="32-bit"):
+            call()
+    with pytest.raises(mm.MegaMoEError):               # within 32 bits the library refuses
+        mm.group_by_expert(idx, 8, first_expert=-1)

@@ -30,3 +30,19 @@ def test_a_result_is_left_alone_where_no_gradient_is_asked_for():
             return 2 * g
     Own.apply(p).sum().backward()
     assert (p.grad == 2).all()
+
+
+def test_sizes_beyond_32_bits_are_refused_and_not_cut():
+    far = (1 << 32) + 8
+    for call in (lambda: ops._weight_bytes(0, far, 8, 1), lambda: ops._weight_bytes(0, 8, far, 1),
+                 lambda: ops._weight_bytes(0, 8, 8, far), lambda: ops._group_bytes(10, far),
+                 lambda: ops._group_bytes(10, 8 - (1 << 32)), lambda: ops._adapter_bytes(1, far, 8, 8, 1, 1),
+                 lambda: ops._adapter_bytes(1, 8, far, 8, 1, 1), lambda: ops._adapter_bytes(1, 8, 8, far, 1, 1),
+                 lambda: ops._adapter_bytes(1, 8, 8, 8, far, 1), lambda: ops._adapter_bytes(1, 8, 8, 8, 1, far)):
+        with pytest.raises(ValueError, match="32-bit"):
+            call()
+    good = (4, 16, 2, 0, 4, 2, 1, 1, 1.0, ops.FP32)
+    assert ops._config(*good).topk == 2
+    for i in (1, 2, 4, 5, 6):
+        with pytest.raises(ValueError, match="32-bit"):
+            ops._config(*good[:i], good[i] + (1 << 32), *good[i + 1:])
