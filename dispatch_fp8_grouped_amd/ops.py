@@ -12,7 +12,8 @@ devices, allocate what they return, and call them.  Everything runs in the HIP k
     y = mm.adapter_forward(x, w, a, b, scales, offsets, adapter)     # one low-rank adapter per request
 
 Tensors must be dense, on one GPU; a slice of tokens that the router or the ordering is given may start anywhere,
-and the other tensors start at a multiple of 16 bytes, as slices of their rows do.  Calls run on the current
+and the other tensors start at a multiple of 16 bytes, as slices of their rows do; `out` and `workspace` share no
+memory with the other tensors.  Calls run on the current
 stream of that GPU, or on `stream` (a torch stream or a stream handle); a tensor that a call returns belongs to the
 stream of the call.  The tensors given with `stream` are recorded on it, so that their memory is not handed out
 again before the call has read it; that they are ready by then is up to the caller, as for any stream.
@@ -248,6 +249,15 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _apart(name, out, *others):
+    """`out` shares no memory with the other tensors of the call: work-groups read them until the last one ends."""
+    first = out.data_ptr()
+    end = first + out.numel() * out.element_size()
+    for t in others:
+        if t is not None and t.data_ptr() < end and first < t.data_ptr() + t.numel() * t.element_size():
+            raise ValueError(f"{name} overlaps another tensor of the call")
+
+
 @functools.lru_cache(None)
 def _stop():
     import torch
@@ -301,6 +311,7 @@ def _grouped(what, rows_in, w, offsets, contract_k, out, status, stream):
             out = torch.empty((rows, outer), dtype=w.dtype, device=w.device)
         else:
             _want("out", out, (rows, outer), (w.dtype,), w.device)
+            _apart("out", out, rows_in, w, offsets, status)
         _mm._check(call(rows_in.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(), rows, n, k, groups,
                         kinds[w.dtype], _at(status), raw), what)
     return out
@@ -348,6 +359,7 @@ def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=Fal
             out = torch.empty((groups, n, k), dtype=dtype, device=x.device)
         else:
             _want("out", out, (groups, n, k), (dtype,), x.device)
+            _apart("out", out, dy, x, offsets, status)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
         _mm._check(_mm.lib().mega_moe_grouped_backward_weight(
             dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), out.data_ptr(), rows, n, k, groups, kinds[x.dtype],
@@ -466,10 +478,12 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
             out = torch.empty((rows, n), dtype=w.dtype, device=w.device)
         else:
             _want("out", out, (rows, n), (w.dtype,), w.device)
+            _apart("out", out, x, w, a, b, scales, offsets, adapter, workspace, status)
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
         else:
             _want("workspace", workspace, None, (torch.uint8,), w.device)
+            _apart("workspace", workspace, x, w, a, b, scales, offsets, adapter, status)
         _mm._check(_mm.lib().mega_moe_adapter_forward(
             x.data_ptr(), w.data_ptr(), a.data_ptr(), b.data_ptr(), scales.data_ptr(), offsets.data_ptr(), adapter.data_ptr(),
             out.data_ptr(), rows, n, k, rank, requests, adapters, kinds[w.dtype], workspace.data_ptr(), workspace.numel(),

@@ -149,3 +149,39 @@ def test_numbers_beyond_32_bits_are_refused():
             call()
     with pytest.raises(mm.MegaMoEError):               # within 32 bits the library refuses
         mm.group_by_expert(idx, 8, first_expert=-1)
+
+
+def test_outputs_and_workspaces_apart_from_the_inputs():
+    args = {n: f() for n, f in case(n=136).items()}
+    pool = torch.zeros(1 << 20, dtype=BF16, device="cuda")
+
+    def place(first, shape):
+        return pool[first:first + shape[0] * shape[1]].view(shape)
+    forward, rows, adapter = args["grouped_forward"], args["grouped_backward_rows"], args["adapter_forward"]
+    with pytest.raises(ValueError, match="out overlaps"):
+        mm.grouped_forward(**forward, out=forward["x"])
+    with pytest.raises(ValueError, match="out overlaps"):
+        mm.grouped_backward_rows(**rows, out=rows["dy"])
+    with pytest.raises(ValueError, match="out overlaps"):
+        mm.adapter_forward(**adapter, out=adapter["x"])
+    # neighbours in one allocation are taken
+    x, out = place(0, (300, 136)), place(300 * 136, (300, 136))
+    x.copy_(forward["x"])
+    want = mm.grouped_forward(**forward)
+    assert torch.equal(mm.grouped_forward(x, forward["w"], forward["offsets"], out=out), want)
+    with pytest.raises(ValueError, match="out overlaps"):
+        mm.grouped_forward(x, forward["w"], forward["offsets"], out=place(299 * 136, (300, 136)))
+    dy = place(0, (300, 136))
+    with pytest.raises(ValueError, match="out overlaps"):
+        mm.grouped_backward_weight(dy, forward["x"], forward["offsets"], accumulate=True,
+                                   out=pool[136 * 299:136 * 299 + 2 * 3 * 136 * 136].view(torch.float32).view(3, 136, 136))
+    need = mm.mega_moe_adapter_workspace_bytes(300, 136, 136, 16, 3)
+    space = torch.empty(need + 300 * 136 * 2, dtype=torch.uint8, device="cuda")
+    out = space[need:].view(BF16).view(300, 136)
+    want = mm.adapter_forward(**adapter)
+    assert torch.equal(mm.adapter_forward(**adapter, out=out, workspace=space[:need]), want)
+    with pytest.raises(ValueError, match="overlaps"):
+        mm.adapter_forward(**adapter, out=out, workspace=space)
+    inside = space[:300 * 136 * 2].view(BF16).view(300, 136)
+    with pytest.raises(ValueError, match="workspace overlaps"):
+        mm.adapter_forward(**{**adapter, "x": inside}, workspace=space)

@@ -46,3 +46,13 @@ def test_sizes_beyond_32_bits_are_refused_and_not_cut():
     for i in (1, 2, 4, 5, 6):
         with pytest.raises(ValueError, match="32-bit"):
             ops._config(*good[:i], good[i] + (1 << 32), *good[i + 1:])
+
+
+def test_outputs_that_share_memory_with_an_input():
+    whole = torch.zeros(100)
+    ops._apart("out", whole[:50], whole[50:], None, torch.zeros(100), torch.zeros(0), whole[10:10])
+    for other in (whole, whole[49:], whole[:1], whole[20:30].view(torch.int32), whole.view(torch.uint8)[199:201]):
+        with pytest.raises(ValueError, match="out overlaps"):
+            ops._apart("out", whole[:50], torch.zeros(3), other)
+    for a, b in ((whole[:50], whole[50:]), (whole[50:], whole[:50])):
+        ops._apart("out", a, b)
