@@ -309,7 +309,7 @@ __device__ __forceinline__ int first_request(const AdapterArgs& g, int m0, int l
     return before;
 }
 
-// y = x w^T + v b^T for one tile.  H: a loop over fewer rows for the last row tile, as in the grouped products.
+// y = x w^T + v b^T for one tile.
 template <class L, class T>
 __device__ __forceinline__ void up_tile(const AdapterArgs& g, int m0, int q0, uint8_t* smem, int wave, int lane) {
     const Operand P{g.x + (size_t)m0 * g.k, g.rows - m0, g.k, g.k}, Q{g.w + (size_t)q0 * g.k, g.n - q0, g.k, g.k};
@@ -355,6 +355,7 @@ __device__ __forceinline__ void up_tile(const AdapterArgs& g, int m0, int q0, ui
     store_halves<L, T>(acc, g.y + (size_t)m0 * g.n + q0, g.rows - m0, g.n - q0, g.n, smem, wave, lane);
 }
 
+// H: a loop over half as many rows for the last row tile, as in the grouped products.
 template <class L, class H, class T, int BM, int BN>
 __global__ __launch_bounds__(L::kThreads) void adapter_up_kernel(AdapterArgs g) {
     static_assert(H::kThreads == L::kThreads, "one launch");

@@ -312,14 +312,16 @@ __device__ __forceinline__ void store_halves(const typename L::Acc (&acc)[L::QI]
 
 // A stream of tiles with two KS operands, for products whose contraction is short beside their output: QuadLoop's
 // steps one tile after the other, the next tile's first two steps loading under the last two of the current one, and
-// the output leaving while the next tile is multiplied.  (A tile per work-group spent as long on its first loads and
-// its stores as on eight steps' MFMAs.)
+// the output's stores completing under the first steps of the next.  (A tile per work-group spent as long on its first
+// loads and its stores as on eight steps' MFMAs.)
 //
 // The waits count instructions, and stores count like loads, in order: after a tile's kStores stores the three waits
 // for groups that were issued before them allow that many more to be outstanding.  So the number of stores of a tile
-// is a constant: the stores of rows or columns that do not exist go past their descriptor's end.
+// is a constant: the stores of rows or columns that do not exist go past their descriptor's end.  Operations retire in
+// order, so the fourth wait, one and a half steps (2 us) into the next tile, is for all of the stores; a CU's share of
+// the fill rate takes about 10 us for a tile's 256 KB of fp32.  Their issue has no MFMA beside it.
 //
-// Tiles: next(first row, first column, contraction length) sets the next tile's operands and output, false at the end.
+// Tiles: next() gives the stream's next tile, made by of(); one without steps is its end.
 template <class T, int kBytes>
 struct KsStream {
     static constexpr int BM = 256, BN = 256;
@@ -490,7 +492,9 @@ struct KsStream {
 // 7168 x 2048 over 32 groups (weights streamed) 215, 212, 201, 188, 191, 204, 204, 240; at 6 x 696 x 2096, one group,
 // 24, 17, 13, 17, 13, 12, 10, 9.
 // Over 56 sizes drawn from 4 to 32768 rows, 1 to 64 groups and 128 to 8192 columns, both directions, the shape picked took
-// 1.5 % longer than the best of them on average and 16 % at most.
+// 1.5 % longer than the best of these shapes on average and 16 % at most.  `fixed` counts once, though every round of
+// tiles has first loads and an epilogue: of a contraction of one or two steps over many rounds the estimate is too
+// low (32768 x 7168 over 8 groups, contraction 64: 32 us estimated, 118 measured, 96 its bytes at a copy's rate).
 struct RowShape {
     int bm, bn, resident;
     double fixed, alone, full;

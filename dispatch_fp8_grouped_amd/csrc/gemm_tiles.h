@@ -91,11 +91,6 @@ __device__ __forceinline__ void wait_vm_barrier() {
     static_assert(N >= 0 && N < 64, "vmcnt immediate");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    static_assert(N >= 0 && N < 64, "vmcnt immediate");
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
 
 // KC: 16-byte chunk c of row r sits at position c ^ kc_swz(r).  A ds_read_b128 is served in four passes of 16
 // lanes, each over all 64 banks: one pass takes eight rows of one lane group's chunk c and the other eight rows

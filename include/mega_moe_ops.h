@@ -58,7 +58,8 @@ extern "C" {
  * backward_weight writes zeros for a group without rows (leaves it as it was when accumulating).
  * With rows == 0, forward and backward_rows do nothing and the row pointers may be NULL.
  * Errors: INVALID_ARG (null or misaligned pointer, negative size), UNSUPPORTED (size or type outside the
- * limits, or an output of more than 2^22 tiles of 128 x 128), WORKSPACE_TOO_SMALL, HIP. */
+ * limits, or an output of more than 2^22 tiles of 128 x 128, a last one per group among them; of the weight gradient,
+ * of more than 2^21 tiles of 256 x 256), WORKSPACE_TOO_SMALL, HIP. */
 int32_t mega_moe_grouped_forward(const void* x, const void* w, const int32_t* offsets, void* y, int64_t rows,
                                  int32_t n, int32_t k, int32_t groups, int32_t dtype, uint32_t* device_status,
                                  void* stream);
@@ -97,8 +98,9 @@ typedef struct mega_moe_router_config {
  *   topk_idx      int64 [T][K]: expert ids, highest rank first; equal ranks: the lower id first.  A token
  *                 with fewer than K experts to choose from gets -1 (no expert) in the places left.
  *   topk_weights  float [T][K]: scale * s, or scale * s / (sum of the chosen s) when renormalizing; 0 where
- *                 topk_idx is -1, and all 0 where the sum is 0 (sigmoid scores of logits below -700; in
- *                 the renormalized softmax the experts that were not chosen cancel out, and it is not)
+ *                 topk_idx is -1, and all 0 where the sum is 0 (sigmoid scores of logits below -709, whose
+ *                 exp(-logit) is beyond fp64; in the renormalized softmax the experts that were not
+ *                 chosen cancel out, and it is not)
  * Rank: s + bias; without a bias the logit itself, whose order is that of s.  With num_groups > 1 only
  * experts of the topk_groups best groups are eligible; a group's worth is the sum of its group_top
  * highest ranks over unmasked experts (without a bias and with group_top 2: of their s), equal worths: the lower
@@ -148,7 +150,8 @@ int32_t mega_moe_group_by_expert(const int64_t* topk_idx, int64_t pairs, int32_t
  * the sum of two 16-bit numbers, the value rounded and the rounded remainder: an error of 2^-16 of it in bf16 and 2^-22
  * in fp16, where a power of two per row and 32 ranks gives it fp32's range (and values below 2^-39 of the largest of
  * their 32 count as 0).
- * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP. */
+ * Errors: INVALID_ARG, UNSUPPORTED (size or type outside the limits, or a y of more than 2^23 tiles of 64 x 128),
+ * WORKSPACE_TOO_SMALL, HIP. */
 int32_t mega_moe_adapter_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t rank, int32_t requests,
                                          uint64_t* bytes_out /* host */);
 int32_t mega_moe_adapter_forward(const void* x, const void* w, const void* a, const void* b, const float* scales,
