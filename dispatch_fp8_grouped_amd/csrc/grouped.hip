@@ -17,6 +17,9 @@
 #include "gemm_kernels.h"
 
 namespace mm {
+
+hipError_t launch_dequantize(const uint8_t* codes, const float* scales, void* y, int rows, int cols, int dtype, hipStream_t st);
+
 namespace {
 
 struct GroupedArgs {
@@ -375,6 +378,30 @@ int32_t mega_moe_grouped_backward_weight(const void* dy, const void* x, const in
     else
         e = dtype == MEGA_MOE_BF16 ? launch_weight<Bf16, false>(a, workspace, st) : launch_weight<Fp16, false>(a, workspace, st);
     return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+}
+
+// Rows kept in 8 bits: restored behind the parts of the sum, then the product above.
+int32_t mega_moe_grouped_codes_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t groups, uint64_t* bytes_out) {
+    const int32_t rc = mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups, bytes_out);
+    if (rc == MEGA_MOE_OK) *bytes_out += (uint64_t)rows * k * 2;
+    return rc;
+}
+
+int32_t mega_moe_grouped_backward_weight_codes(const void* dy, const uint8_t* codes, const float* scales, const int32_t* offsets,
+                                               void* dw, int64_t rows, int32_t n, int32_t k, int32_t groups, int32_t dtype,
+                                               int32_t out_dtype, int32_t accumulate, void* workspace, uint64_t workspace_bytes,
+                                               uint32_t* device_status, void* stream) {
+    const int32_t rc = check_grouped(dy, workspace, offsets, dw, rows, n, k, groups, dtype, device_status, true);
+    if (rc) return rc;
+    if (rows > 0 && (!codes || !scales || ((uintptr_t)scales & 3u))) return MEGA_MOE_ERR_INVALID_ARG;
+    uint64_t need = 0;
+    mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups, &need);
+    if (workspace_bytes < need + (uint64_t)rows * k * 2) return MEGA_MOE_ERR_WORKSPACE_TOO_SMALL;
+    void* x = static_cast<char*>(workspace) + need;
+    if (rows > 0 && launch_dequantize(codes, scales, x, (int)rows, k, dtype, static_cast<hipStream_t>(stream)) != hipSuccess)
+        return MEGA_MOE_ERR_HIP;
+    return mega_moe_grouped_backward_weight(dy, x, offsets, dw, rows, n, k, groups, dtype, out_dtype, accumulate, workspace, need,
+                                            device_status, stream);
 }
 
 }  // extern "C"

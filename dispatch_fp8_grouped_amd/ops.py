@@ -1,5 +1,6 @@
 """Operators around the fused MoE layer (include/mega_moe_ops.h): products grouped by expert and their
-gradients, the router with its gradient and the ordering of its pairs, and adapter projections.
+gradients, the router with its gradient and the ordering of its pairs, adapter projections, the root-mean-square norm and
+SwiGLU with their gradients, and activations in 8 bits.
 
 The functions with the C names marshal arguments only; the short names below them check shapes, types and
 devices, allocate what they return, and call them.  Everything runs in the HIP kernels of libmegamoe.so.
@@ -10,18 +11,26 @@ devices, allocate what they return, and call them.  Everything runs in the HIP k
     dx = mm.grouped_backward_rows(dy, w, offsets)
     dw = mm.grouped_backward_weight(dy, x_sorted, offsets)
     y = mm.adapter_forward(x, w, a, b, scales, offsets, adapter)     # one low-rank adapter per request
+    y, h, rows8 = mm.rms_norm(x, weight, residual=h, quantize="both")   # rows8 = (codes, scales): MegaMoE's x and x_sf
+    act, kept = mm.swiglu(gate_up, checkpoint=True)                  # kept: gate_up in 8 bits for the backward pass
+    dgate_up, act = mm.swiglu_backward(dact, kept, recompute=True)
+    dw = mm.grouped_backward_weight(dgate_up, rows8, offsets)        # from rows kept in 8 bits
+    dx, dweight = mm.rms_norm_backward(dy, h, weight, dresidual=dh)
 
-Tensors must be dense, on one GPU; a slice of tokens that the router or the ordering is given may start anywhere,
-and the other tensors start at a multiple of 16 bytes, as slices of their rows do; `out` and `workspace` share no
-memory with the other tensors.  Calls run on the current
+Tensors must be dense, on one GPU; a slice of tokens that the router or the ordering is given may start anywhere, so may
+the rows of the norm, of SwiGLU and in 8 bits, and the other tensors start at a multiple of 16 bytes, as slices of their
+rows do; `out` and `workspace` share no memory with the other tensors.  Calls run on the current
 stream of that GPU, or on `stream` (a torch stream or a stream handle); a tensor that a call returns belongs to the
 stream of the call.  The tensors given with `stream` are recorded on it, so that their memory is not handed out
 again before the call has read it; that they are ready by then is up to the caller, as for any stream.
 
 The functions compute values and gradients; autograd does not derive the one from the other.  Where it records and
-an input requires a gradient, what grouped_forward, router_topk (its weights) and adapter_forward return carries a node
-that raises in backward(), so that no parameter goes without its gradient unnoticed; what the gradient calls return,
-and what is written into `out`, is recorded nowhere.
+an input requires a gradient, what grouped_forward, router_topk (its weights), adapter_forward, rms_norm (y and h), swiglu
+(act) and dequantize_rows return carries a node that raises in backward(), so that no parameter goes without its gradient
+unnoticed; what the gradient calls return, what is kept in 8 bits, and what is written into `out`, is recorded nowhere.
+
+Rows in 8 bits are a pair (codes uint8 [..., cols], scales float32 [..., ceil(cols / 128)]) of e4m3 codes and a scale per
+128 columns, as MegaMoE takes its tokens; the scales that are written here are powers of two.
 """
 from __future__ import annotations
 
@@ -41,12 +50,16 @@ _SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
 OPS_EXPORTS = ("mega_moe_grouped_forward", "mega_moe_grouped_backward_rows", "mega_moe_grouped_backward_weight",
                "mega_moe_grouped_weight_workspace_bytes",
                "mega_moe_router_topk", "mega_moe_router_backward", "mega_moe_group_workspace_bytes",
-               "mega_moe_group_by_expert", "mega_moe_adapter_workspace_bytes", "mega_moe_adapter_forward")
+               "mega_moe_group_by_expert", "mega_moe_adapter_workspace_bytes", "mega_moe_adapter_forward",
+               "mega_moe_quantize_rows", "mega_moe_dequantize_rows", "mega_moe_grouped_codes_workspace_bytes",
+               "mega_moe_grouped_backward_weight_codes", "mega_moe_rms_norm", "mega_moe_norm_workspace_bytes",
+               "mega_moe_rms_norm_backward", "mega_moe_swiglu", "mega_moe_swiglu_backward")
 
 
 __all__ = ["BF16", "FP16", "FP32", "SCORE_SOFTMAX", "SCORE_SIGMOID", "OPS_EXPORTS", *OPS_EXPORTS,
            "grouped_forward", "grouped_backward_rows", "grouped_backward_weight", "mega_moe_router_config",
-           "router_topk", "router_backward", "group_by_expert", "adapter_forward"]
+           "router_topk", "router_backward", "group_by_expert", "adapter_forward",
+           "quantize_rows", "dequantize_rows", "rms_norm", "rms_norm_backward", "swiglu", "swiglu_backward"]
 
 
 class mega_moe_router_config(ctypes.Structure):
@@ -71,6 +84,16 @@ def _bind(L):
     L.mega_moe_group_by_expert.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, u64, vp]
     L.mega_moe_adapter_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, ctypes.POINTER(u64)]
     L.mega_moe_adapter_forward.argtypes = [vp] * 8 + [i64] + [i32] * 6 + [vp, u64, vp, vp]
+    f32 = ctypes.c_float
+    L.mega_moe_quantize_rows.argtypes = [vp, vp, vp, i64, i32, i32, vp]
+    L.mega_moe_dequantize_rows.argtypes = [vp, vp, vp, i64, i32, i32, vp]
+    L.mega_moe_grouped_codes_workspace_bytes.argtypes = [i64, i32, i32, i32, ctypes.POINTER(u64)]
+    L.mega_moe_grouped_backward_weight_codes.argtypes = [vp] * 5 + [i64] + [i32] * 6 + [vp, u64, vp, vp]
+    L.mega_moe_rms_norm.argtypes = [vp] * 7 + [i64, i32, f32, i32, i32, i32, vp]
+    L.mega_moe_norm_workspace_bytes.argtypes = [i64, i32, ctypes.POINTER(u64)]
+    L.mega_moe_rms_norm_backward.argtypes = [vp] * 7 + [i64, i32, f32, i32, i32, i32, vp, u64, vp]
+    L.mega_moe_swiglu.argtypes = [vp] * 5 + [i32, i64, i32, i32, vp, vp]
+    L.mega_moe_swiglu_backward.argtypes = [vp] * 6 + [i32, i64, i32, i32, vp, vp]
     for name in OPS_EXPORTS:
         getattr(L, name).restype = i32
 
@@ -148,6 +171,70 @@ def mega_moe_adapter_forward(x, w, a, b, scales, offsets, adapter, y, rows, n, k
                                                 _mm._ptr(device_status), _mm._stream(stream)), "mega_moe_adapter_forward")
 
 
+def mega_moe_quantize_rows(x, codes, scales, rows, cols, dtype, stream=None):
+    _mm._check(_mm.lib().mega_moe_quantize_rows(_mm._ptr(x), _mm._ptr(codes), _mm._ptr(scales), rows, cols, dtype,
+                                                _mm._stream(stream)), "mega_moe_quantize_rows")
+
+
+def mega_moe_dequantize_rows(codes, scales, y, rows, cols, dtype, stream=None):
+    _mm._check(_mm.lib().mega_moe_dequantize_rows(_mm._ptr(codes), _mm._ptr(scales), _mm._ptr(y), rows, cols, dtype,
+                                                  _mm._stream(stream)), "mega_moe_dequantize_rows")
+
+
+def mega_moe_grouped_codes_workspace_bytes(rows: int, n: int, k: int, groups: int) -> int:
+    out = ctypes.c_uint64(0)
+    _mm._check(_mm.lib().mega_moe_grouped_codes_workspace_bytes(rows, n, k, groups, ctypes.byref(out)),
+               "mega_moe_grouped_codes_workspace_bytes")
+    return out.value
+
+
+def mega_moe_grouped_backward_weight_codes(dy, codes, scales, offsets, dw, rows, n, k, groups, dtype, out_dtype,
+                                           accumulate=False, workspace=None, workspace_bytes=None, device_status=None,
+                                           stream=None):
+    nbytes = workspace_bytes
+    if nbytes is None:
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _mm._check(_mm.lib().mega_moe_grouped_backward_weight_codes(
+        _mm._ptr(dy), _mm._ptr(codes), _mm._ptr(scales), _mm._ptr(offsets), _mm._ptr(dw), rows, n, k, groups, dtype, out_dtype,
+        1 if accumulate else 0, _mm._ptr(workspace), nbytes, _mm._ptr(device_status), _mm._stream(stream)),
+        "mega_moe_grouped_backward_weight_codes")
+
+
+def mega_moe_rms_norm(x, residual, weight, h, y, codes, scales, rows, hidden, eps, dtype, residual_dtype, weight_dtype,
+                      stream=None):
+    _mm._check(_mm.lib().mega_moe_rms_norm(_mm._ptr(x), _mm._ptr(residual), _mm._ptr(weight), _mm._ptr(h), _mm._ptr(y),
+                                           _mm._ptr(codes), _mm._ptr(scales), rows, hidden, eps, dtype, residual_dtype,
+                                           weight_dtype, _mm._stream(stream)), "mega_moe_rms_norm")
+
+
+def mega_moe_norm_workspace_bytes(rows: int, hidden: int) -> int:
+    out = ctypes.c_uint64(0)
+    _mm._check(_mm.lib().mega_moe_norm_workspace_bytes(rows, hidden, ctypes.byref(out)), "mega_moe_norm_workspace_bytes")
+    return out.value
+
+
+def mega_moe_rms_norm_backward(dy, h, h_scales, weight, dresidual, dx, dweight, rows, hidden, eps, dtype, residual_dtype,
+                               weight_dtype, workspace, workspace_bytes=None, stream=None):
+    nbytes = workspace_bytes if workspace_bytes is not None else workspace.numel() * workspace.element_size()
+    _mm._check(_mm.lib().mega_moe_rms_norm_backward(
+        _mm._ptr(dy), _mm._ptr(h), _mm._ptr(h_scales), _mm._ptr(weight), _mm._ptr(dresidual), _mm._ptr(dx), _mm._ptr(dweight), rows,
+        hidden, eps, dtype, residual_dtype, weight_dtype, _mm._ptr(workspace), nbytes, _mm._stream(stream)),
+        "mega_moe_rms_norm_backward")
+
+
+def mega_moe_swiglu(gate_up, act, codes, scales, offsets, groups, rows, inter, dtype, device_status=None, stream=None):
+    _mm._check(_mm.lib().mega_moe_swiglu(_mm._ptr(gate_up), _mm._ptr(act), _mm._ptr(codes), _mm._ptr(scales),
+                                         _mm._ptr(offsets), groups, rows, inter, dtype, _mm._ptr(device_status),
+                                         _mm._stream(stream)), "mega_moe_swiglu")
+
+
+def mega_moe_swiglu_backward(dact, gate_up, scales, dgate_up, act, offsets, groups, rows, inter, dtype, device_status=None,
+                             stream=None):
+    _mm._check(_mm.lib().mega_moe_swiglu_backward(_mm._ptr(dact), _mm._ptr(gate_up), _mm._ptr(scales), _mm._ptr(dgate_up),
+                                                  _mm._ptr(act), _mm._ptr(offsets), groups, rows, inter, dtype,
+                                                  _mm._ptr(device_status), _mm._stream(stream)), "mega_moe_swiglu_backward")
+
+
 # --------------------------------------------------------------- checks
 def _int32(**sizes):
     """Each of them fits the library's int32: ctypes would pass its low 32 bits without a word."""
@@ -175,6 +262,18 @@ def _adapter_bytes(rows, n, k, rank, requests, adapters):
     return mega_moe_adapter_workspace_bytes(rows, n, k, rank, requests)
 
 
+@functools.lru_cache(1024)
+def _codes_bytes(rows, n, k, groups):
+    _int32(n=n, k=k, groups=groups)
+    return mega_moe_grouped_codes_workspace_bytes(rows, n, k, groups)
+
+
+@functools.lru_cache(1024)
+def _norm_bytes(rows, hidden):
+    _int32(hidden=hidden)
+    return mega_moe_norm_workspace_bytes(rows, hidden)
+
+
 def _want(name, t, shape, dtypes, device=None):
     """t is a dense GPU tensor of this shape and one of these types (shape None: any)."""
     if (t is not None and t.is_cuda and t.is_contiguous() and t.dtype in dtypes
@@ -191,6 +290,15 @@ def _want(name, t, shape, dtypes, device=None):
 def _current():
     import torch
     return torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _want_codes(name, codes, scales, device=None):
+    """Rows in 8 bits: codes uint8 [..., cols] and scales float32 [..., ceil(cols / 128)]."""
+    import torch
+    _want(f"{name} (codes)", codes, None, (torch.uint8,), device)
+    if codes.dim() < 1 or codes.shape[-1] < 1:
+        raise ValueError(f"{name} (codes): want [..., cols], got {tuple(codes.shape)}")
+    _want(f"{name} (scales)", scales, (*codes.shape[:-1], -(-codes.shape[-1] // 128)), (torch.float32,), codes.device)
 
 
 class _Call:
@@ -335,36 +443,52 @@ def grouped_backward_rows(dy, w, offsets, out=None, status=None, stream=None):
 
 def grouped_backward_weight(dy, x, offsets, dtype=None, out=None, accumulate=False, status=None, stream=None):
     """dw[e] = dy_e.T @ x_e: the gradient of grouped_forward's weights, [groups, n, k] in `dtype` (the
-    operands', or float32).  A group without rows gets zeros.  With accumulate, `out` (float32) is added to."""
+    operands', or float32).  A group without rows gets zeros.  With accumulate, `out` (float32) is added to.
+    x: rows, or a pair (codes, scales) of rows kept in 8 bits, whose values enter the product in dy's type."""
     import torch
     kinds = _halves()
-    _want("x", x, None, kinds)
+    codes = scales = None
+    if isinstance(x, tuple):
+        codes, scales = x
+        _want_codes("x", codes, scales)
+        x = codes
+    else:
+        _want("x", x, None, kinds)
     if x.dim() != 2 or dy is None or dy.dim() != 2 or offsets is None or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("grouped_backward_weight: want dy [rows, n], x [rows, k] and offsets [groups + 1]")
     rows, k = x.shape
     n, groups = dy.shape[1], offsets.numel() - 1
-    _want("dy", dy, (rows, n), (x.dtype,), x.device)
+    if codes is None:
+        kind = x.dtype
+        _want("dy", dy, (rows, n), (kind,), x.device)
+    else:
+        kind = dy.dtype
+        _want("dy", dy, (rows, n), kinds, x.device)
     _want("offsets", offsets, (groups + 1,), (torch.int32,), x.device)
     if dtype is None:
-        dtype = out.dtype if out is not None else x.dtype
-    if dtype not in (x.dtype, torch.float32):
-        raise ValueError(f"dtype: want {x.dtype} or torch.float32, got {dtype}")
+        dtype = out.dtype if out is not None else kind
+    if dtype not in (kind, torch.float32):
+        raise ValueError(f"dtype: want {kind} or torch.float32, got {dtype}")
     if accumulate and (out is None or dtype != torch.float32):
         raise ValueError("accumulate needs a float32 `out`")
     if status is not None:
         _want("status", status, (1,), (torch.int32,), x.device)
-    nbytes = _weight_bytes(rows, n, k, groups)
-    with _Call(x.device, stream, dy, x, offsets, out, status) as raw:
+    nbytes = (_weight_bytes if codes is None else _codes_bytes)(rows, n, k, groups)
+    with _Call(x.device, stream, dy, x, scales, offsets, out, status) as raw:
         if out is None:
             out = torch.empty((groups, n, k), dtype=dtype, device=x.device)
         else:
             _want("out", out, (groups, n, k), (dtype,), x.device)
-            _apart("out", out, dy, x, offsets, status)
+            _apart("out", out, dy, x, scales, offsets, status)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
-        _mm._check(_mm.lib().mega_moe_grouped_backward_weight(
-            dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), out.data_ptr(), rows, n, k, groups, kinds[x.dtype],
-            FP32 if dtype == torch.float32 else kinds[dtype], 1 if accumulate else 0, _at(workspace), nbytes, _at(status),
-            raw), "grouped_backward_weight")
+        sizes = (offsets.data_ptr(), out.data_ptr(), rows, n, k, groups, kinds[kind],
+                 FP32 if dtype == torch.float32 else kinds[dtype], 1 if accumulate else 0, _at(workspace), nbytes, _at(status),
+                 raw)
+        if codes is None:
+            rc = _mm.lib().mega_moe_grouped_backward_weight(dy.data_ptr(), x.data_ptr(), *sizes)
+        else:
+            rc = _mm.lib().mega_moe_grouped_backward_weight_codes(dy.data_ptr(), codes.data_ptr(), scales.data_ptr(), *sizes)
+        _mm._check(rc, "grouped_backward_weight")
     return out
 
 
@@ -489,3 +613,194 @@ def adapter_forward(x, w, a, b, scales, offsets, adapter, out=None, workspace=No
             out.data_ptr(), rows, n, k, rank, requests, adapters, kinds[w.dtype], workspace.data_ptr(), workspace.numel(),
             _at(status), raw), "adapter_forward")
     return _unrecorded("adapter_forward", "it serves adapters and has no gradient", out, x, w, a, b, scales) if fresh else out
+
+
+def _rows(name, t, device=None):
+    """Rows of float32, bfloat16 or float16: (rows, cols)"""
+    _want(name, t, None, _logit_kinds(), device)
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name}: want [..., cols], got {tuple(t.shape)}")
+    cols = t.shape[-1]
+    if cols >> 31:
+        _int32(cols=cols)
+    return t.numel() // cols, cols
+
+
+def quantize_rows(x, stream=None):
+    """x [..., cols] (bfloat16, float16 or float32) in 8 bits: (codes uint8 [..., cols], scales float32 [..., ceil(cols /
+    128)]), one scale per row and 128 columns, the smallest power of two that saturates no value.  A block of 128 that
+    holds an infinity or a NaN becomes NaN.  See mega_moe_ops.h."""
+    import torch
+    rows, cols = _rows("x", x)
+    with _Call(x.device, stream, x) as raw:
+        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        scales = torch.empty((*x.shape[:-1], -(-cols // 128)), dtype=torch.float32, device=x.device)
+        _mm._check(_mm.lib().mega_moe_quantize_rows(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, cols,
+                                                    _logit_kinds()[x.dtype], raw), "quantize_rows")
+    return codes, scales
+
+
+def dequantize_rows(codes, scales, dtype=None, stream=None):
+    """The values of rows in 8 bits, codes * scales, in `dtype` (bfloat16, float16 or float32; default bfloat16)."""
+    import torch
+    kinds = _logit_kinds()
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in kinds:
+        raise ValueError(f"dtype: want one of {sorted(map(str, kinds))}, got {dtype}")
+    _want_codes("rows", codes, scales)
+    cols = codes.shape[-1]
+    if cols >> 31:
+        _int32(cols=cols)
+    with _Call(codes.device, stream, codes, scales) as raw:
+        y = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+        _mm._check(_mm.lib().mega_moe_dequantize_rows(codes.data_ptr(), scales.data_ptr(), y.data_ptr(), codes.numel() // cols,
+                                                      cols, kinds[dtype], raw), "dequantize_rows")
+    return _unrecorded("dequantize_rows", "the rounding to 8 bits has none", y, scales)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False, dtype=None, stream=None):
+    """Root-mean-square norm of x + residual: (y, h, rows8).
+
+    h = x + residual, of the residual's type, None without one; y = (x + residual) * weight / sqrt(mean of its squares +
+    eps), in `dtype`; rows8 = (codes, scales) of y in 8 bits, as MegaMoE takes x and x_sf.  quantize: False (y alone,
+    rows8 None), True (rows8 alone, y None) or "both".
+    x [..., hidden] bfloat16, float16 or float32; residual of x's type or float32; weight [hidden] of y's type or float32;
+    dtype x's, or, for a float32 x without a residual (a residual stream as it stands), any of the three."""
+    import torch
+    if quantize not in (False, True, "both"):
+        raise ValueError(f'quantize: want False, True or "both", got {quantize!r}')
+    kinds = _logit_kinds()
+    rows, hidden = _rows("x", x)
+    device, given = x.device, x
+    dtype = x.dtype if dtype is None else dtype
+    if dtype not in kinds or (dtype != x.dtype and (residual is not None or x.dtype != torch.float32)):
+        raise ValueError(f"dtype: want {x.dtype}, or another of a float32 x without a residual, got {dtype}")
+    _want("weight", weight, (hidden,), (dtype, torch.float32), device)
+    if residual is not None:
+        _want("residual", residual, x.shape, (x.dtype, torch.float32), device)
+    with _Call(device, stream, x, weight, residual) as raw:
+        h = None if residual is None else torch.empty(x.shape, dtype=residual.dtype, device=device)
+        y = torch.empty(x.shape, dtype=dtype, device=device) if quantize is not True else None
+        codes = scales = None
+        if quantize:
+            codes = torch.empty(x.shape, dtype=torch.uint8, device=device)
+            scales = torch.empty((*x.shape[:-1], -(-hidden // 128)), dtype=torch.float32, device=device)
+        # a stream as it stands goes in as the residual, which may have another type than y
+        first, second = (x, residual) if residual is not None or x.dtype == dtype else (None, x)
+        _mm._check(_mm.lib().mega_moe_rms_norm(
+            _at(first), _at(second), weight.data_ptr(), _at(h), _at(y), _at(codes), _at(scales), rows, hidden, eps, kinds[dtype],
+            kinds[dtype if second is None else second.dtype], kinds[weight.dtype], raw), "rms_norm")
+    how = "compute its gradients with rms_norm_backward"
+    if y is not None:
+        y = _unrecorded("rms_norm", how, y, given, weight, *(() if residual is None else (residual,)))
+    if h is not None:
+        h = _unrecorded("rms_norm", how, h, given, residual)
+    return y, h, None if codes is None else (codes, scales)
+
+
+def rms_norm_backward(dy, h, weight, eps=1e-6, dresidual=None, stream=None):
+    """(dx, dweight float32 [hidden]) of rms_norm: dx is the gradient of x + residual, and so of both, with dresidual (what
+    reached h from elsewhere) added.
+
+    dy of y's type; h: what was normalised (rms_norm's h, or x without a residual), of dy's type or float32, or a pair
+    (codes, scales) of it kept in 8 bits; dresidual of h's type (of dy's or float32 with an h in 8 bits).  dx has dresidual's
+    type, else h's, else dy's."""
+    import torch
+    kinds = _logit_kinds()
+    rows, hidden = _rows("dy", dy)
+    device = dy.device
+    if isinstance(h, tuple):
+        values, scales = h
+        _want_codes("h", values, scales, device)
+        if values.shape != dy.shape:
+            raise ValueError(f"h (codes): want {tuple(dy.shape)}, got {tuple(values.shape)}")
+        kind = dy.dtype if dresidual is None else dresidual.dtype
+    else:
+        values, scales = h, None
+        _want("h", h, dy.shape, (dy.dtype, torch.float32), device)
+        kind = h.dtype
+    _want("weight", weight, (hidden,), (dy.dtype, torch.float32), device)
+    if dresidual is not None:
+        _want("dresidual", dresidual, dy.shape, (kind,) if scales is None else (dy.dtype, torch.float32), device)
+    nbytes = _norm_bytes(rows, hidden)
+    with _Call(device, stream, dy, values, scales, weight, dresidual) as raw:
+        dx = torch.empty(dy.shape, dtype=kind, device=device)
+        dweight = torch.empty(hidden, dtype=torch.float32, device=device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        _mm._check(_mm.lib().mega_moe_rms_norm_backward(
+            dy.data_ptr(), values.data_ptr(), _at(scales), weight.data_ptr(), _at(dresidual), dx.data_ptr(), dweight.data_ptr(), rows,
+            hidden, eps, kinds[dy.dtype], kinds[kind], kinds[weight.dtype], _at(workspace), nbytes, raw), "rms_norm_backward")
+    return dx, dweight
+
+
+def _swiglu_sizes(what, t, name, factor):
+    """rows and inter of t [rows, factor * inter]"""
+    if t is None or t.dim() != 2 or t.shape[1] < factor or t.shape[1] % factor:
+        raise ValueError(f"{what}: want {name} [rows, {'2 inter' if factor == 2 else 'inter'}]"
+                         f"{'' if t is None else ', got ' + str(tuple(t.shape))}")
+    if t.shape[1] >> 31:
+        _int32(cols=t.shape[1])
+    return t.shape[0], t.shape[1] // factor
+
+
+def _swiglu_groups(offsets, status, device):
+    import torch
+    if status is not None:
+        _want("status", status, (1,), (torch.int32,), device)
+    if offsets is None:
+        return 0
+    _want("offsets", offsets, None, (torch.int32,), device)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets: want [groups + 1]")
+    return offsets.numel() - 1
+
+
+def swiglu(gate_up, checkpoint=False, offsets=None, status=None, stream=None):
+    """(act, kept): act = silu(gate) * up of the rows (gate, up) of gate_up [rows, 2 inter], bfloat16 or float16.
+
+    With checkpoint, kept = (codes uint8 [rows, 2 inter], scales float32 [rows, 2 ceil(inter / 128)]): gate_up in 8 bits for
+    swiglu_backward, gate and up each as a row of its own; else None.  offsets: int32 [groups + 1] of the grouped
+    products, or None; rows of no group are neither read nor written."""
+    import torch
+    kinds = _halves()
+    _want("gate_up", gate_up, None, kinds)
+    rows, inter = _swiglu_sizes("swiglu", gate_up, "gate_up", 2)
+    device = gate_up.device
+    groups = _swiglu_groups(offsets, status, device)
+    with _Call(device, stream, gate_up, offsets, status) as raw:
+        act = torch.empty((rows, inter), dtype=gate_up.dtype, device=device)
+        codes = scales = None
+        if checkpoint:
+            codes = torch.empty(gate_up.shape, dtype=torch.uint8, device=device)
+            scales = torch.empty((rows, 2 * -(-inter // 128)), dtype=torch.float32, device=device)
+        _mm._check(_mm.lib().mega_moe_swiglu(gate_up.data_ptr(), act.data_ptr(), _at(codes), _at(scales), _at(offsets), groups,
+                                             rows, inter, kinds[gate_up.dtype], _at(status), raw), "swiglu")
+    act = _unrecorded("swiglu", "compute its gradient with swiglu_backward", act, gate_up)
+    return act, None if codes is None else (codes, scales)
+
+
+def swiglu_backward(dact, gate_up, recompute=False, offsets=None, status=None, stream=None):
+    """(dgate_up [rows, 2 inter], act): the gradient of swiglu's rows, and with recompute act again (else None), for the
+    gradient of the weights that it was multiplied with.
+
+    dact [rows, inter] bfloat16 or float16; gate_up of the same type, or what swiglu kept of it in 8 bits."""
+    import torch
+    kinds = _halves()
+    _want("dact", dact, None, kinds)
+    rows, inter = _swiglu_sizes("swiglu_backward", dact, "dact", 1)
+    device = dact.device
+    if isinstance(gate_up, tuple):
+        values, scales = gate_up
+        _want("gate_up (codes)", values, (rows, 2 * inter), (torch.uint8,), device)
+        _want("gate_up (scales)", scales, (rows, 2 * -(-inter // 128)), (torch.float32,), device)
+    else:
+        values, scales = gate_up, None
+        _want("gate_up", gate_up, (rows, 2 * inter), (dact.dtype,), device)
+    groups = _swiglu_groups(offsets, status, device)
+    with _Call(device, stream, dact, values, scales, offsets, status) as raw:
+        dgate_up = torch.empty((rows, 2 * inter), dtype=dact.dtype, device=device)
+        act = torch.empty((rows, inter), dtype=dact.dtype, device=device) if recompute else None
+        _mm._check(_mm.lib().mega_moe_swiglu_backward(
+            dact.data_ptr(), values.data_ptr(), _at(scales), dgate_up.data_ptr(), _at(act), _at(offsets), groups, rows, inter,
+            kinds[dact.dtype], _at(status), raw), "swiglu_backward")
+    return dgate_up, act

@@ -4,7 +4,9 @@
  *   - the router: choosing and weighing the experts of every token (topk_idx / topk_weights as
  *     mega_moe_forward takes them), its gradient, and the ordering of the chosen pairs by expert that
  *     the grouped products read;
- *   - a projection shared by many requests that each bring a low-rank adapter.
+ *   - a projection shared by many requests that each bring a low-rank adapter;
+ *   - the root-mean-square norm in front of the layer, in 16 and in 8 bits, and its gradient;
+ *   - SwiGLU between the experts' products and its gradient, and activations kept in 8 bits for the backward pass.
  *
  * Conventions are those of mega_moe.h: 0 or a negative MEGA_MOE_ERR_* code, nothing throws; device
  * pointers (16-byte aligned unless the comment says otherwise), dense row-major tensors; work is enqueued
@@ -35,6 +37,7 @@ extern "C" {
 #define MEGA_MOE_MAX_GROUP_COLS 65536       /* its n and k */
 #define MEGA_MOE_MAX_PAIRS 2147418112       /* 2^31 - 2^16: chosen (token, expert) pairs */
 #define MEGA_MOE_MAX_REQUESTS 4096          /* requests of an adapter projection */
+#define MEGA_MOE_MAX_NORM_COLS 16384        /* columns of a normalised row */
 
 /* ------------------------------------------------------------------ products grouped by expert
  * Rows are sorted by group: group e owns rows offsets[e] .. offsets[e+1]-1 of the row tensors (any count,
@@ -158,6 +161,91 @@ int32_t mega_moe_adapter_forward(const void* x, const void* w, const void* a, co
                                  const int32_t* offsets, const int32_t* adapter, void* y, int64_t rows, int32_t n,
                                  int32_t k, int32_t rank, int32_t requests, int32_t adapters, int32_t dtype,
                                  void* workspace, uint64_t workspace_bytes, uint32_t* device_status, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit rows
+ * Rows in 8 bits as the layer takes its tokens: codes uint8 [rows][cols] (e4m3fn) and scales float [rows][ceil(cols / 128)],
+ * one per row and 128 columns (the last block may be shorter); the value is code * scale.  Every scale that is written
+ * here is a power of two, 2^ceil(log2(largest / 448)) of the largest magnitude of its block (2^-126 at least): no value
+ * saturates, each is rounded once to four significant bits (to nearest, ties to even; below 2^-6 scales to multiples of
+ * 2^-9 scales; what would become 2^128 becomes 1.875 * 2^127), and code * scale is exact in bf16 and fp16.  A block that holds an infinity or a NaN becomes NaN
+ * throughout, with scale 1.  Scales that are read may be any numbers.
+ * The row operators below take rows of any length from 1 on, and pointers that are aligned to their element type
+ * (codes: to nothing).
+ *   quantize_rows    x dtype [rows][cols] -> codes, scales
+ *   dequantize_rows  codes, scales -> y dtype [rows][cols], rounded to dtype where that has fewer bits (fp16: 65536, to which
+ *                    four bits round fp16's largest numbers, comes back as 65504)
+ *   rows   0 .. MEGA_MOE_MAX_GROUP_ROWS (pointers may be NULL at 0), cols 1 .. MEGA_MOE_MAX_GROUP_COLS
+ *   dtype  MEGA_MOE_BF16, _FP16 or _FP32
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP. */
+int32_t mega_moe_quantize_rows(const void* x, uint8_t* codes, float* scales, int64_t rows, int32_t cols, int32_t dtype, void* stream);
+int32_t mega_moe_dequantize_rows(const uint8_t* codes, const float* scales, void* y, int64_t rows, int32_t cols, int32_t dtype,
+                                 void* stream);
+
+/* The weight gradient of the grouped products from rows kept in 8 bits:
+ *   dw[e] = sum over the rows m of group e of dy[m]^T x[m],   x[m] = codes * scales
+ *   dy dtype [rows][n], codes uint8 [rows][k], scales float [rows][ceil(k / 128)].  A value enters the product in dtype:
+ *   exactly with scales that are powers of two, unless it leaves fp16's range (as in dequantize_rows), else rounded.
+ * Everything else, the limits and errors included, as for mega_moe_grouped_backward_weight, but codes and scales need not be
+ * aligned beyond their type, and
+ *   workspace  mega_moe_grouped_codes_workspace_bytes() bytes */
+int32_t mega_moe_grouped_codes_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t groups, uint64_t* bytes_out /* host */);
+int32_t mega_moe_grouped_backward_weight_codes(const void* dy, const uint8_t* codes, const float* scales, const int32_t* offsets,
+                                               void* dw, int64_t rows, int32_t n, int32_t k, int32_t groups, int32_t dtype,
+                                               int32_t out_dtype, int32_t accumulate, void* workspace, uint64_t workspace_bytes,
+                                               uint32_t* device_status, void* stream);
+
+/* ------------------------------------------------------------------ norm
+ * Root-mean-square norm of rows, with the residual's addition:
+ *   v = x + residual,  h = v rounded,  y = v w / sqrt(mean over the row of v^2 + eps)
+ *   x         dtype [rows][hidden], or NULL: v = residual (a residual stream of its own type, without an addition)
+ *   residual  residual_dtype [rows][hidden], or NULL: v = x
+ *   weight    weight_dtype [hidden]
+ *   h         residual_dtype [rows][hidden] or NULL; y dtype [rows][hidden] or NULL; codes and scales (8-bit rows of y) or
+ *             both NULL; at least one of the three
+ *   dtype     MEGA_MOE_BF16, _FP16 or _FP32; residual_dtype, weight_dtype: dtype or MEGA_MOE_FP32
+ *   rows 0 .. MEGA_MOE_MAX_GROUP_ROWS (pointers may be NULL at 0), hidden 1 .. MEGA_MOE_MAX_NORM_COLS; eps >= 0, finite
+ * v and the sums are fp32; y and the codes are computed from v, not from h, and rounded once each.  Squares beyond fp32's
+ * range (values from 1.8e19 on) give y = 0.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP. */
+int32_t mega_moe_rms_norm(const void* x, const void* residual, const void* weight, void* h, void* y, uint8_t* codes, float* scales,
+                          int64_t rows, int32_t hidden, float eps, int32_t dtype, int32_t residual_dtype, int32_t weight_dtype,
+                          void* stream);
+
+/* Its gradient: with r = 1 / sqrt(mean h^2 + eps), n = h r and g = dy w,
+ *   dx = r (g - n mean(g n)) + dresidual,   dweight = sum over the rows of dy n
+ * dx is the gradient of v, and so of x and of residual alike; dresidual is what reached h from elsewhere.
+ *   dy         dtype [rows][hidden]
+ *   h          residual_dtype [rows][hidden] with h_scales NULL, or codes with their h_scales (8-bit rows)
+ *   dresidual  residual_dtype [rows][hidden] or NULL; dx residual_dtype [rows][hidden]; dweight float [hidden]
+ *   workspace  mega_moe_norm_workspace_bytes() bytes, 4-byte aligned (may be NULL with rows 0); its contents do not matter
+ * With rows 0 dweight is zeros.  Sums are fp32, dweight's in an order that depends on the sizes alone.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP. */
+int32_t mega_moe_norm_workspace_bytes(int64_t rows, int32_t hidden, uint64_t* bytes_out /* host */);
+int32_t mega_moe_rms_norm_backward(const void* dy, const void* h, const float* h_scales, const void* weight, const void* dresidual,
+                                   void* dx, float* dweight, int64_t rows, int32_t hidden, float eps, int32_t dtype,
+                                   int32_t residual_dtype, int32_t weight_dtype, void* workspace, uint64_t workspace_bytes,
+                                   void* stream);
+
+/* ------------------------------------------------------------------ SwiGLU
+ * Between the experts' two products: a row of gate_up is gate | up, inter columns each,
+ *   act = gate / (1 + exp(-gate)) * up
+ *   gate_up  dtype [rows][2 inter], act dtype [rows][inter]; dtype MEGA_MOE_BF16 or MEGA_MOE_FP16
+ *   codes    uint8 [rows][2 inter] and scales float [rows][2][ceil(inter / 128)], or both NULL: gate_up in 8 bits for the
+ *            backward pass; gate and up are 8-bit rows of their own
+ *   offsets  int32 [groups + 1] as for the grouped products, or NULL (all rows): only rows offsets[0] .. offsets[groups]-1 are
+ *            read and written; entries outside 0 .. rows are clamped and latch MEGA_MOE_STATUS_BAD_LAYOUT
+ *   rows 0 .. MEGA_MOE_MAX_GROUP_ROWS (pointers may be NULL at 0), inter 1 .. MEGA_MOE_MAX_GROUP_COLS
+ * backward, with s = 1 / (1 + exp(-gate)):
+ *   dgate = dact up s (1 + gate (1 - s)),  dup = dact gate s  -> dgate_up dtype [rows][2 inter]
+ *   gate_up  dtype [rows][2 inter] with scales NULL, or codes with their scales
+ *   act      dtype [rows][inter] or NULL: act again, for the gradient of the second product's weights
+ * Arithmetic is fp32, every output rounded once.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP. */
+int32_t mega_moe_swiglu(const void* gate_up, void* act, uint8_t* codes, float* scales, const int32_t* offsets, int32_t groups,
+                        int64_t rows, int32_t inter, int32_t dtype, uint32_t* device_status, void* stream);
+int32_t mega_moe_swiglu_backward(const void* dact, const void* gate_up, const float* scales, void* dgate_up, void* act,
+                                 const int32_t* offsets, int32_t groups, int64_t rows, int32_t inter, int32_t dtype,
+                                 uint32_t* device_status, void* stream);
 
 #ifdef __cplusplus
 }
