@@ -36,16 +36,16 @@ struct Walk {
 
 __device__ __forceinline__ void keep(uint8_t* codes, float* scales, int64_t row, int block, int blocks, int cols, int c, float (&v)[8]) {
     const Scale s(max16(largest(v)));
-    s.store(codes, (size_t)row * cols + c, cols - c, v);
+    s.store<false>(codes, (size_t)row * cols + c, cols - c, v);
     if ((threadIdx.x & 15) == 0) scales[(size_t)row * blocks + block] = s.scale;
 }
 
-template <class T>
+template <class T, bool kOnce>
 __global__ __launch_bounds__(256) void quantize_kernel(const void* x, uint8_t* codes, float* scales, int rows, int cols) {
     for (Walk w(scale_blocks(cols), 0); w.row < rows; w.next()) {
         const int c = w.block * kScaleCols + (threadIdx.x & 15) * 8;
         float v[8];
-        Row8<T>::load(x, (size_t)w.row * cols + c, cols - c).get(v);
+        Row8<T>::template load<kOnce>(x, (size_t)w.row * cols + c, cols - c).get(v);
         keep(codes, scales, w.row, w.block, w.blocks, cols, c, v);
     }
 }
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, c
     for (Walk w(scale_blocks(cols), 0); w.row < rows; w.next()) {
         const int c = w.block * kScaleCols + (threadIdx.x & 15) * 8;
         float v[8];
-        Codes8::load(codes, (size_t)w.row * cols + c, cols - c).get(scales[(size_t)w.row * w.blocks + w.block], v);
+        Codes8::load<false>(codes, (size_t)w.row * cols + c, cols - c).get(scales[(size_t)w.row * w.blocks + w.block], v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = restored<T>(v[i]);
         Row8<T>::store(y, (size_t)w.row * cols + c, cols - c, v);
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel<Fp32>(const uint8_t* co
     for (Walk w(scale_blocks(cols), 0); w.row < rows; w.next()) {
         const int c = w.block * kScaleCols + (threadIdx.x & 15) * 8;
         float v[8];
-        Codes8::load(codes, (size_t)w.row * cols + c, cols - c).get(scales[(size_t)w.row * w.blocks + w.block], v);
+        Codes8::load<false>(codes, (size_t)w.row * cols + c, cols - c).get(scales[(size_t)w.row * w.blocks + w.block], v);
         Row8<Fp32>::store(y, (size_t)w.row * cols + c, cols - c, v);
     }
 }
@@ -103,21 +103,22 @@ __device__ __forceinline__ void used_rows(const SwigluArgs& a, int& lo, int& hi)
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
-template <class T>
+template <class T, bool kKeep, bool kOnce>
 __global__ __launch_bounds__(256) void swiglu_kernel(SwigluArgs a) {
     int lo, hi;
     used_rows(a, lo, hi);
     for (Walk w(scale_blocks(a.inter), lo); w.row < hi; w.next()) {
         const int c = w.block * kScaleCols + (threadIdx.x & 15) * 8, n = a.inter - c;
         const size_t at = (size_t)w.row * a.inter;
-        const Row8<T> gate = Row8<T>::load(a.gate_up, 2 * at + c, n), up = Row8<T>::load(a.gate_up, 2 * at + a.inter + c, n);
+        const Row8<T> gate = Row8<T>::template load<kOnce>(a.gate_up, 2 * at + c, n);
+        const Row8<T> up = Row8<T>::template load<kOnce>(a.gate_up, 2 * at + a.inter + c, n);
         float g[8], u[8], y[8];
         gate.get(g);
         up.get(u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = g[i] * sigmoid(g[i]) * u[i];
         Row8<T>::store(a.act, at + c, n, y);
-        if (a.codes) {      // gate and up are kept as rows of their own
+        if constexpr (kKeep) {      // gate and up are kept as rows of their own
             keep(a.codes, a.scales, 2 * w.row, w.block, w.blocks, a.inter, c, g);
             keep(a.codes, a.scales, 2 * w.row + 1, w.block, w.blocks, a.inter, c, u);
         }
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(256) void swiglu_grad_kernel(SwigluArgs a) {
         float d[8], g[8], u[8], y[8];
         if constexpr (kCodes) {
             const float* s = a.in_scales + (size_t)w.row * 2 * w.blocks + w.block;
-            const Codes8 gate = Codes8::load(a.gate_up, 2 * at + c, n), up = Codes8::load(a.gate_up, 2 * at + a.inter + c, n);
+            const Codes8 gate = Codes8::load<true>(a.gate_up, 2 * at + c, n), up = Codes8::load<true>(a.gate_up, 2 * at + a.inter + c, n);
             gate.get(s[0], g);
             up.get(s[w.blocks], u);
         } else {
@@ -161,6 +162,25 @@ __global__ __launch_bounds__(256) void swiglu_grad_kernel(SwigluArgs a) {
 dim3 walk_grid(int64_t rows, int cols) {
     const int64_t n = (rows * scale_blocks(cols) + 15) / 16;
     return dim3((uint32_t)(n < 4096 ? n : 4096));
+}
+
+template <class T>
+hipError_t launch_quantize(const void* x, uint8_t* codes, float* scales, int rows, int cols, hipStream_t st) {
+    const dim3 grid = walk_grid(rows, cols);
+    if (beyond_cache((uint64_t)rows * cols * Row8<T>::kBytes))
+        hipLaunchKernelGGL((quantize_kernel<T, true>), grid, dim3(256), 0, st, x, codes, scales, rows, cols);
+    else
+        hipLaunchKernelGGL((quantize_kernel<T, false>), grid, dim3(256), 0, st, x, codes, scales, rows, cols);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t st) {
+    const dim3 grid = walk_grid(a.rows, a.inter);
+    if (!a.codes) hipLaunchKernelGGL((swiglu_kernel<T, false, false>), grid, dim3(256), 0, st, a);
+    else if (beyond_cache((uint64_t)a.rows * a.inter * 4)) hipLaunchKernelGGL((swiglu_kernel<T, true, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((swiglu_kernel<T, true, false>), grid, dim3(256), 0, st, a);
+    return hipGetLastError();
 }
 
 bool half(int32_t dtype) { return dtype == MEGA_MOE_BF16 || dtype == MEGA_MOE_FP16; }
@@ -199,12 +219,11 @@ int32_t mega_moe_quantize_rows(const void* x, uint8_t* codes, float* scales, int
     if (!rows_supported(rows, cols) || (!half(dtype) && dtype != MEGA_MOE_FP32)) return MEGA_MOE_ERR_UNSUPPORTED;
     if (rows == 0) return MEGA_MOE_OK;
     if (!element(x, dtype) || !codes || !word(scales)) return MEGA_MOE_ERR_INVALID_ARG;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    const dim3 grid = walk_grid(rows, cols);
-    if (dtype == MEGA_MOE_BF16) hipLaunchKernelGGL((quantize_kernel<Bf16>), grid, dim3(256), 0, st, x, codes, scales, (int)rows, cols);
-    else if (dtype == MEGA_MOE_FP16) hipLaunchKernelGGL((quantize_kernel<Fp16>), grid, dim3(256), 0, st, x, codes, scales, (int)rows, cols);
-    else hipLaunchKernelGGL((quantize_kernel<Fp32>), grid, dim3(256), 0, st, x, codes, scales, (int)rows, cols);
-    return hipGetLastError() == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+    hipError_t e;
+    if (dtype == MEGA_MOE_BF16) e = launch_quantize<Bf16>(x, codes, scales, (int)rows, cols, static_cast<hipStream_t>(stream));
+    else if (dtype == MEGA_MOE_FP16) e = launch_quantize<Fp16>(x, codes, scales, (int)rows, cols, static_cast<hipStream_t>(stream));
+    else e = launch_quantize<Fp32>(x, codes, scales, (int)rows, cols, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
 int32_t mega_moe_dequantize_rows(const uint8_t* codes, const float* scales, void* y, int64_t rows, int32_t cols, int32_t dtype, void* stream) {
@@ -224,10 +243,8 @@ int32_t mega_moe_swiglu(const void* gate_up, void* act, uint8_t* codes, float* s
     if (!element(gate_up, dtype) || !element(act, dtype) || (codes != nullptr) != (scales != nullptr) || ((uintptr_t)scales & 3u))
         return MEGA_MOE_ERR_INVALID_ARG;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const dim3 grid = walk_grid(rows, inter);
-    if (dtype == MEGA_MOE_BF16) hipLaunchKernelGGL((swiglu_kernel<Bf16>), grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL((swiglu_kernel<Fp16>), grid, dim3(256), 0, st, a);
-    return hipGetLastError() == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
+    const hipError_t e = dtype == MEGA_MOE_BF16 ? launch_swiglu<Bf16>(a, st) : launch_swiglu<Fp16>(a, st);
+    return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
 int32_t mega_moe_swiglu_backward(const void* dact, const void* gate_up, const float* scales, void* dgate_up, void* act,

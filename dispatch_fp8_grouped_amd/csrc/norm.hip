@@ -4,6 +4,8 @@
 //   backward   r as above from h, n = h r, g = dy w:  dx = r (g - n mean(g n)) + dresidual,  dw = sum over rows of dy n
 // One pass over memory: a row stays in the registers of its lanes between its reduction and its outputs.  All arithmetic
 // is fp32; y and the codes come from the unrounded sum v, each with its one rounding.
+#include <type_traits>
+
 #include "row_io.h"
 
 namespace mm {
@@ -15,7 +17,7 @@ struct NormArgs {
     uint8_t* codes;                      // may be null
     float* scales;
     int rows, hidden, weight_fp32;
-    float eps;
+    double mean, eps;                    // 1 / hidden
 };
 
 // Eight weights from column c on: fp32 or of type T.
@@ -25,27 +27,33 @@ __device__ __forceinline__ void weights8(const void* w, int fp32, int c, int n, 
     else Row8<T>::load(w, c, n).get(v);
 }
 
-// The sum over the lanes of a row.  kLanes 16 or 64: within the wave.  0: the whole work-group, through LDS that alternates
+// Sums over the lanes of a row.  kLanes 16 or 64: within the wave.  0: the whole work-group, through LDS that alternates
 // between two buffers from row to row, so that one barrier a row is enough: a buffer is written again only after the
-// barrier of the row in between.
+// barrier of the row in between.  A lane adds its few values in fp32 and the lanes are joined in fp64: r is then known to
+// half a step of fp32: its error is that of every value of the row, and moves some over the borders of the 8-bit grid.
 template <int kLanes, int kSums>
-__device__ __forceinline__ void row_sums(float (&v)[kSums], float (*lds)[kSums], int turn) {
+__device__ __forceinline__ void row_sums(double (&v)[kSums], double (*lds)[kSums], int turn) {
 #pragma unroll
     for (int i = 0; i < kSums; ++i) v[i] = kLanes == 16 ? sum16(v[i]) : sum64(v[i]);
     if constexpr (kLanes == 0) {
         const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-        float(*at)[kSums] = lds + turn * 16;
+        double(*at)[kSums] = lds + turn * 16;
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
             for (int i = 0; i < kSums; ++i) at[wave][i] = v[i];
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSums; ++i) v[i] = 0.f;
+        for (int i = 0; i < kSums; ++i) v[i] = 0.0;
         for (int w = 0; w < waves; ++w)
 #pragma unroll
             for (int i = 0; i < kSums; ++i) v[i] += at[w][i];
     }
+}
+// 1 / sqrt(a), with one Newton step from the hardware's estimate; 0 and infinity, and NaN, as they come from it.
+__device__ __forceinline__ double inverse_root(double a) {
+    const double r = __builtin_amdgcn_rsq(a);
+    return a > 0.0 && a < __builtin_inf() ? r * (1.5 - 0.5 * a * r * r) : r;
 }
 
 // Where a lane stands: its row within the work-group, its place among the row's lanes, and their number.
@@ -63,7 +71,7 @@ struct Place {
 // T: x, y (and weight); R: residual, h.  A row's units of 8 columns go to its lanes in turn, kUnits to each.
 template <class T, class R, int kLanes, int kUnits>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs a) {
-    __shared__ float lds[32][1];
+    __shared__ double lds[32][1];
     const Place<kLanes> p;
     int turn = 0;
     for (int row = blockIdx.x * p.rows + p.row; row < a.rows; row += gridDim.x * p.rows, turn ^= 1) {
@@ -76,7 +84,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
             x[u] = Row8<T>::load(a.x, at + c, a.x ? a.hidden - c : 0);
             res[u] = Row8<R>::load(a.residual, at + c, a.residual ? a.hidden - c : 0);
         }
-        float v[kUnits][8], sum[1] = {0.f};
+        float v[kUnits][8], squares = 0.f;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int c = (u * p.lanes + p.lane) * 8;
@@ -86,23 +94,30 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[u][i] += r[i];
-                sum[0] += v[u][i] * v[u][i];
+                squares += v[u][i] * v[u][i];
             }
             if (a.h) Row8<R>::store(a.h, at + c, a.hidden - c, v[u]);
         }
+        double sum[1] = {squares};
         row_sums<kLanes>(sum, lds, turn);
-        const float r = 1.0f / sqrtf(sum[0] / (float)a.hidden + a.eps);
+        // y = v (r w) with what r and r w lose added to the product: within half a step of fp32 of v r w.  The number of values
+        // that fall on the other side of an 8-bit border is proportional to that error, and the pass takes as long (353 us).
+        const double root = inverse_root(sum[0] * a.mean + a.eps);
+        const float r = (float)root, lost = root < __builtin_inf() ? (float)(root - (double)r) : 0.f;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int c = (u * p.lanes + p.lane) * 8, n = a.hidden - c;
             float w[8];
             weights8<T>(a.weight, a.weight_fp32, c, n, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] *= r * w[i];
+            for (int i = 0; i < 8; ++i) {
+                const float rw = r * w[i], less = __builtin_fmaf(lost, w[i], __builtin_fmaf(r, w[i], -rw));
+                v[u][i] = __builtin_fmaf(v[u][i], rw, v[u][i] * less);
+            }
             if (a.y) Row8<T>::store(a.y, at + c, n, v[u]);
             if (a.codes) {
                 const Scale s(max16(largest(v[u])));
-                s.store(a.codes, at + c, n, v[u]);
+                s.template store<true>(a.codes, at + c, n, v[u]);
                 if ((p.lane & 15) == 0 && n > 0) a.scales[(size_t)row * scale_blocks(a.hidden) + c / kScaleCols] = s.scale;
             }
         }
@@ -115,58 +130,93 @@ struct NormGradArgs {
     void* dx;
     float* partial;                            // [gridDim.x][hidden]
     int rows, hidden, weight_fp32;
-    float eps;
+    double mean, eps;                          // 1 / hidden
 };
 
-// T: dy (and weight); R: dresidual, dx, and h unless kCodes.
-template <class T, class R, bool kCodes, int kLanes, int kUnits>
+// What a lane holds of a row as it is in memory.  T: dy; R: dresidual, and h unless kCodes.
+template <class T, class R, bool kCodes, bool kOnce, int kUnits>
+struct GradRow {
+    Row8<T> dy[kUnits];
+    typename std::conditional<kCodes, Codes8, Row8<R>>::type h[kUnits];
+    float scale[kUnits];
+    Row8<R> dres[kUnits];
+    __device__ __forceinline__ void load(const NormGradArgs& a, int row, int lane, int lanes) {
+        const size_t at = (size_t)row * a.hidden;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int c = (u * lanes + lane) * 8, n = row < a.rows ? a.hidden - c : 0;
+            dy[u] = Row8<T>::template load<kOnce>(a.dy, at + c, n);
+            h[u] = h[u].template load<kOnce>(a.h, at + c, n);
+            scale[u] = 0.f;
+            if (kCodes && n > 0) scale[u] = a.scales[(size_t)row * scale_blocks(a.hidden) + c / kScaleCols];
+            dres[u] = Row8<R>::template load<kOnce>(a.dresidual, at + c, a.dresidual ? n : 0);
+        }
+    }
+    // What was converted for the sums is converted again for dx: the fp32 values of both passes would take twice the registers.
+    __device__ __forceinline__ void keep_packed() {
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            dy[u].opaque();
+            h[u].opaque();
+        }
+    }
+    __device__ __forceinline__ void values(int u, float (&v)[8], float (&w)[8]) const {
+        dy[u].get(v);
+        if constexpr (kCodes) h[u].get(scale[u], w);
+        else h[u].get(w);
+    }
+};
+
+// T: dy (and weight); R: dresidual, dx, and h unless kCodes.  The next row is on its way while one is reduced and written.
+template <class T, class R, bool kCodes, bool kOnce, int kLanes, int kUnits>
 __global__ __launch_bounds__(kLanes ? 256 : 512) void rms_norm_grad_kernel(NormGradArgs a) {
-    __shared__ float lds[32][2];
+    __shared__ double lds[32][2];
     const Place<kLanes> p;
     float dw[kUnits][8];
 #pragma unroll
     for (int u = 0; u < kUnits; ++u)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[u][i] = 0.f;
-    int turn = 0;
-    for (int row = blockIdx.x * p.rows + p.row; row < a.rows; row += gridDim.x * p.rows, turn ^= 1) {
+    int turn = 0, row = blockIdx.x * p.rows + p.row;
+    const int step = gridDim.x * p.rows;
+    // (four units a lane leave no registers for the next row)
+    constexpr bool kAhead = kUnits <= 2;
+    GradRow<T, R, kCodes, kOnce, kUnits> next;
+    if (kAhead) next.load(a, row, p.lane, p.lanes);
+    for (; row < a.rows; row += step, turn ^= 1) {
         const size_t at = (size_t)row * a.hidden;
-        float dy[kUnits][8], h[kUnits][8], sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const int c = (u * p.lanes + p.lane) * 8, n = a.hidden - c;
-            Row8<T>::load(a.dy, at + c, n).get(dy[u]);
-            if constexpr (kCodes) {
-                const float s = n > 0 ? a.scales[(size_t)row * scale_blocks(a.hidden) + c / kScaleCols] : 0.f;
-                Codes8::load(a.h, at + c, n).get(s, h[u]);
-            } else {
-                Row8<R>::load(a.h, at + c, n).get(h[u]);
-            }
-        }
+        if (!kAhead) next.load(a, row, p.lane, p.lanes);
+        GradRow<T, R, kCodes, kOnce, kUnits> here = next;
+        if (kAhead) next.load(a, row + step, p.lane, p.lanes);
+        float squares = 0.f, products = 0.f;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int c = (u * p.lanes + p.lane) * 8;
-            float w[8];
+            float w[8], dy[8], h[8];
             weights8<T>(a.weight, a.weight_fp32, c, a.hidden - c, w);
+            here.values(u, dy, h);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sum[0] += h[u][i] * h[u][i];
-                sum[1] += dy[u][i] * w[i] * h[u][i];
+                squares += h[i] * h[i];
+                products += dy[i] * w[i] * h[i];
             }
         }
+        double sum[2] = {squares, products};
         row_sums<kLanes>(sum, lds, turn);
-        const float r = 1.0f / sqrtf(sum[0] / (float)a.hidden + a.eps), m = sum[1] / (float)a.hidden * r;   // mean(g n)
+        const float r = (float)inverse_root(sum[0] * a.mean + a.eps), m = (float)(sum[1] * a.mean) * r;   // mean(g n)
+        here.keep_packed();
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int c = (u * p.lanes + p.lane) * 8, n = a.hidden - c;
-            float w[8], d[8], dres[8];
+            float w[8], d[8], dy[8], h[8];
             weights8<T>(a.weight, a.weight_fp32, c, n, w);
-            Row8<R>::load(a.dresidual, at + c, a.dresidual ? n : 0).get(dres);
+            here.values(u, dy, h);
+            here.dres[u].get(d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float nv = h[u][i] * r;
-                d[i] = r * (dy[u][i] * w[i] - nv * m) + dres[i];
-                dw[u][i] += dy[u][i] * nv;
+                const float nv = h[i] * r;
+                d[i] += r * (dy[i] * w[i] - nv * m);
+                dw[u][i] += dy[i] * nv;
             }
             Row8<R>::store(a.dx, at + c, n, d);
         }
@@ -209,8 +259,11 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* partial, f
     __shared__ float lds[32][33];
     const int col = threadIdx.x & 31, run = threadIdx.x >> 5, c = blockIdx.x * 32 + col, per = (parts + 31) / 32;
     float v = 0.f;
-    if (c < hidden)
-        for (int i = run * per; i < min(parts, (run + 1) * per); ++i) v += partial[(size_t)i * hidden + c];
+    if (c < hidden) {
+        const int end = min(parts, (run + 1) * per);
+#pragma unroll 8
+        for (int i = run * per; i < end; ++i) v += partial[(size_t)i * hidden + c];
+    }
     lds[run][col] = v;
     __syncthreads();
     if (run) return;
@@ -227,17 +280,21 @@ RowShape8 row_shape(int hidden, int max_threads) {
     const int n = (hidden + 7) / 8;
     if (n <= 16) return {16, 1, 256, 16};
     if (n <= 64) return {64, 1, 256, 4};
+    if (n <= 128) return {64, 2, 256, 4};
     if (n <= 256) return {64, 4, 256, 4};
     int units = 2;
     while ((n + units - 1) / units > max_threads) units *= 2;
     return {0, units, ((n + units - 1) / units + 63) / 64 * 64, 1};
 }
 
-// work-groups of a launch: a partial sum of dw each, so no more than fill the CUs twice
+// Work-groups of the gradient, which have a partial sum of dw each: those that are resident at once, 16 waves to a CU by the
+// registers (32768 rows: 7168 columns, 7 waves: 374 us with 512, 423 with 256, 378 with 1024 and 416 with 2048; 4096
+// columns, 4 waves: 223 with 512, 211 with 1024).
 int grad_blocks(int64_t rows, int hidden) {
     const RowShape8 s = row_shape(hidden, 512);
     const int64_t n = (rows + s.rows - 1) / s.rows;
-    return (int)(n < 512 ? n : 512);
+    const int64_t most = 256 * (16 / (s.threads / 64));
+    return (int)(n < most ? n : most);
 }
 
 template <class T, class R, int kLanes, int kUnits>
@@ -251,21 +308,25 @@ template <class T, class R>
 hipError_t launch_norm(const NormArgs& a, hipStream_t st) {
     const RowShape8 s = row_shape(a.hidden, 1024);
     if (s.lanes == 16) return launch_norm_with<T, R, 16, 1>(a, s, st);
-    if (s.lanes == 64) return s.units == 1 ? launch_norm_with<T, R, 64, 1>(a, s, st) : launch_norm_with<T, R, 64, 4>(a, s, st);
+    if (s.lanes == 64 && s.units == 1) return launch_norm_with<T, R, 64, 1>(a, s, st);
+    if (s.lanes == 64) return s.units == 2 ? launch_norm_with<T, R, 64, 2>(a, s, st) : launch_norm_with<T, R, 64, 4>(a, s, st);
     return launch_norm_with<T, R, 0, 2>(a, s, st);
 }
 
 template <class T, class R, bool kCodes, int kLanes, int kUnits>
 hipError_t launch_grad_with(const NormGradArgs& a, const RowShape8& s, hipStream_t st) {
-    hipLaunchKernelGGL((rms_norm_grad_kernel<T, R, kCodes, kLanes, kUnits>), dim3((uint32_t)grad_blocks(a.rows, a.hidden)),
-                       dim3(s.threads), 0, st, a);
+    const dim3 grid((uint32_t)grad_blocks(a.rows, a.hidden)), threads(s.threads);
+    const uint64_t each = (uint64_t)a.rows * a.hidden, bytes = each * (Row8<T>::kBytes + (kCodes ? 1 : Row8<R>::kBytes) + (a.dresidual ? Row8<R>::kBytes : 0));
+    if (beyond_cache(bytes)) hipLaunchKernelGGL((rms_norm_grad_kernel<T, R, kCodes, true, kLanes, kUnits>), grid, threads, 0, st, a);
+    else hipLaunchKernelGGL((rms_norm_grad_kernel<T, R, kCodes, false, kLanes, kUnits>), grid, threads, 0, st, a);
     return hipGetLastError();
 }
 template <class T, class R, bool kCodes>
 hipError_t launch_grad(const NormGradArgs& a, hipStream_t st) {
     const RowShape8 s = row_shape(a.hidden, 512);
     if (s.lanes == 16) return launch_grad_with<T, R, kCodes, 16, 1>(a, s, st);
-    if (s.lanes == 64) return s.units == 1 ? launch_grad_with<T, R, kCodes, 64, 1>(a, s, st) : launch_grad_with<T, R, kCodes, 64, 4>(a, s, st);
+    if (s.lanes == 64 && s.units == 1) return launch_grad_with<T, R, kCodes, 64, 1>(a, s, st);
+    if (s.lanes == 64) return s.units == 2 ? launch_grad_with<T, R, kCodes, 64, 2>(a, s, st) : launch_grad_with<T, R, kCodes, 64, 4>(a, s, st);
     return s.units == 2 ? launch_grad_with<T, R, kCodes, 0, 2>(a, s, st) : launch_grad_with<T, R, kCodes, 0, 4>(a, s, st);
 }
 template <bool kCodes>
@@ -303,7 +364,7 @@ int32_t mega_moe_rms_norm(const void* x, const void* residual, const void* weigh
     if (!aligned(x, dtype) || !aligned(residual, residual_dtype) || !aligned(weight, weight_dtype) || !aligned(h, residual_dtype) ||
         !aligned(y, dtype) || !aligned4(scales))
         return MEGA_MOE_ERR_INVALID_ARG;
-    const NormArgs a{x, residual, weight, h, y, codes, scales, (int)rows, hidden, weight_dtype == MEGA_MOE_FP32, eps};
+    const NormArgs a{x, residual, weight, h, y, codes, scales, (int)rows, hidden, weight_dtype == MEGA_MOE_FP32, 1.0 / hidden, eps};
     hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e;
     if (dtype == MEGA_MOE_FP32) e = launch_norm<Fp32, Fp32>(a, st);
@@ -338,7 +399,7 @@ int32_t mega_moe_rms_norm_backward(const void* dy, const void* h, const float* h
     const int blocks = grad_blocks(rows, hidden);
     if (rows > 0) {
         const NormGradArgs a{dy, h, weight, dresidual, h_scales, dx, static_cast<float*>(workspace), (int)rows, hidden,
-                             weight_dtype == MEGA_MOE_FP32, eps};
+                             weight_dtype == MEGA_MOE_FP32, 1.0 / hidden, eps};
         const hipError_t e = h_scales ? launch_grad_types<true>(a, dtype, residual_dtype, st) : launch_grad_types<false>(a, dtype, residual_dtype, st);
         if (e != hipSuccess) return MEGA_MOE_ERR_HIP;
     }

@@ -22,17 +22,32 @@ typedef u32x4 u32x4_any __attribute__((aligned(2)));      // 16 bytes at an addr
 typedef u32x4 u32x4_any4 __attribute__((aligned(4)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 
+// Loads and stores that leave the caches to others (non-temporal) or not.  Rows are written past the caches everywhere:
+// 32768 rows of 2048 columns in SwiGLU 76 -> 58 us, of 7168 columns in the norm 372 -> 353, restored 133 -> 105, and what reads
+// them next takes no longer (SwiGLU and the product behind it 302 -> 296 us at 8192 rows, 850 and 854 at 32768).
+template <bool kOnce, class V>
+__device__ __forceinline__ V read(const V* p) {
+    if constexpr (kOnce) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool kOnce, class V, class W>
+__device__ __forceinline__ void write(V* p, W v) {
+    if constexpr (kOnce) __builtin_nontemporal_store((V)v, p);
+    else *p = v;
+}
+
 // Eight values as they are in memory, and the way to them: load n >= 8 at once, or the n < 8 that exist with zeros
-// behind them (n <= 0 reads nothing).
+// behind them (n <= 0 reads nothing).  opaque(): what was computed from them before is not known to the compiler any more.
 template <class T>
 struct Row8 {
     static constexpr int kBytes = 2;
     u32x4 w;
+    template <bool kOnce = false>
     static __device__ __forceinline__ Row8 load(const void* base, size_t at, int n) {
         const uint16_t* p = static_cast<const uint16_t*>(base) + at;
         Row8 r;
         if (n >= 8) {
-            r.w = *reinterpret_cast<const u32x4_any*>(p);
+            r.w = read<kOnce>(reinterpret_cast<const u32x4_any*>(p));
         } else {
             r.w = u32x4{0, 0, 0, 0};
 #pragma unroll
@@ -41,6 +56,7 @@ struct Row8 {
         }
         return r;
     }
+    __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -54,7 +70,7 @@ struct Row8 {
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] = T::pack(v[2 * i], v[2 * i + 1]);
         if (n >= 8) {
-            *reinterpret_cast<u32x4_any*>(p) = r;
+            write<true>(reinterpret_cast<u32x4_any*>(p), r);
         } else {
 #pragma unroll
             for (int i = 0; i < 7; ++i)
@@ -66,12 +82,13 @@ template <>
 struct Row8<Fp32> {
     static constexpr int kBytes = 4;
     u32x4 a, b;
+    template <bool kOnce = false>
     static __device__ __forceinline__ Row8 load(const void* base, size_t at, int n) {
         const uint32_t* p = static_cast<const uint32_t*>(base) + at;
         Row8 r;
         if (n >= 8) {
-            r.a = *reinterpret_cast<const u32x4_any4*>(p);
-            r.b = *reinterpret_cast<const u32x4_any4*>(p + 4);
+            r.a = read<kOnce>(reinterpret_cast<const u32x4_any4*>(p));
+            r.b = read<kOnce>(reinterpret_cast<const u32x4_any4*>(p + 4));
         } else {
             r.a = r.b = u32x4{0, 0, 0, 0};
 #pragma unroll
@@ -80,6 +97,7 @@ struct Row8<Fp32> {
         }
         return r;
     }
+    __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(a), "+v"(b)); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -96,8 +114,8 @@ struct Row8<Fp32> {
                 lo[i] = __float_as_uint(v[i]);
                 hi[i] = __float_as_uint(v[4 + i]);
             }
-            *reinterpret_cast<u32x4_any4*>(p) = lo;
-            *reinterpret_cast<u32x4_any4*>(p + 4) = hi;
+            write<true>(reinterpret_cast<u32x4_any4*>(p), lo);
+            write<true>(reinterpret_cast<u32x4_any4*>(p + 4), hi);
         } else {
 #pragma unroll
             for (int i = 0; i < 7; ++i)
@@ -109,11 +127,12 @@ struct Row8<Fp32> {
 // Eight codes; get() multiplies by their scale.
 struct Codes8 {
     u32x2 w;
+    template <bool kOnce>
     static __device__ __forceinline__ Codes8 load(const void* base, size_t at, int n) {
         const uint8_t* p = static_cast<const uint8_t*>(base) + at;
         Codes8 r;
         if (n >= 8) {
-            r.w = *reinterpret_cast<const u32x2_any*>(p);
+            r.w = read<kOnce>(reinterpret_cast<const u32x2_any*>(p));
         } else {
             r.w = u32x2{0, 0};
 #pragma unroll
@@ -122,6 +141,7 @@ struct Codes8 {
         }
         return r;
     }
+    __device__ __forceinline__ void opaque() { asm volatile("" : "+v"(w)); }
     __device__ __forceinline__ void get(float scale, float (&v)[8]) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -133,6 +153,7 @@ struct Codes8 {
         }
     }
     // v / scale in codes, inverse = 1 / scale (exact, a power of two): at most 448 in magnitude, or NaN
+    template <bool kOnce>
     static __device__ __forceinline__ void store(void* base, size_t at, int n, const float (&v)[8], float inverse) {
         uint8_t* p = static_cast<uint8_t*>(base) + at;
         u32x2 r;
@@ -142,7 +163,7 @@ struct Codes8 {
             r[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inverse, v[4 * i + 3] * inverse, lo, true);
         }
         if (n >= 8) {
-            *reinterpret_cast<u32x2_any*>(p) = r;
+            write<kOnce>(reinterpret_cast<u32x2_any*>(p), r);
         } else {
 #pragma unroll
             for (int i = 0; i < 7; ++i)
@@ -162,14 +183,19 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
     v = max(v, turned<2>(v));
     return max(v, turned<1>(v));
 }
-// The same bits in all 16 lanes: after each step the values repeat with half the period, and additions commute.
-__device__ __forceinline__ float sum16(float v) {
-    v += __uint_as_float(turned<8>(__float_as_uint(v)));
-    v += __uint_as_float(turned<4>(__float_as_uint(v)));
-    v += __uint_as_float(turned<2>(__float_as_uint(v)));
-    return v + __uint_as_float(turned<1>(__float_as_uint(v)));
+template <int kBy>
+__device__ __forceinline__ double turned(double v) {
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    return __builtin_bit_cast(double, u32x2{turned<kBy>(w[0]), turned<kBy>(w[1])});
 }
-__device__ __forceinline__ float sum64(float v) {
+// The same bits in all lanes: after each step the values repeat with half the period, and additions commute.
+__device__ __forceinline__ double sum16(double v) {
+    v += turned<8>(v);
+    v += turned<4>(v);
+    v += turned<2>(v);
+    return v + turned<1>(v);
+}
+__device__ __forceinline__ double sum64(double v) {
     v = sum16(v);
     v += __shfl_xor(v, 16);
     return v + __shfl_xor(v, 32);
@@ -196,15 +222,21 @@ struct Scale {
         inverse = __uint_as_float(finite ? (uint32_t)(254 - e) << 23 : 0x7FC00000u);
     }
     // codes of eight values; at the very end of fp32's range the largest four-bit number below 2^128 stands for what is above it
+    template <bool kOnce>
     __device__ __forceinline__ void store(void* codes, size_t at, int n, float (&v)[8]) const {
         if (end) {
             const float most = __uint_as_float(0x7F700000u);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = v[i] > most ? most : v[i] < -most ? -most : v[i];
         }
-        Codes8::store(codes, at, n, v, inverse);
+        Codes8::store<kOnce>(codes, at, n, v, inverse);
     }
 };
+
+// Whether a pass reads more than the last-level cache holds (256 MB): what it reads is then in no cache, and is read past
+// them.  Measured past them and not: 32768 rows, quantize of 7168 columns 119 and 132 us, the norm's gradient 354 and
+// 362, SwiGLU of 2048 with its input kept 85 and 90; 4096 rows, read while they are in the cache: 17.6 and 15.7, 48 and 42, 14 and 12.
+inline bool beyond_cache(uint64_t bytes) { return bytes > (uint64_t)256 << 20; }
 
 constexpr int kScaleCols = 128;      // columns of one scale
 __host__ __device__ inline int scale_blocks(int cols) { return (cols + kScaleCols - 1) / kScaleCols; }

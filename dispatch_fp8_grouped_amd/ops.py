@@ -633,7 +633,7 @@ def quantize_rows(x, stream=None):
     import torch
     rows, cols = _rows("x", x)
     with _Call(x.device, stream, x) as raw:
-        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        codes = torch.empty_like(x, dtype=torch.uint8)
         scales = torch.empty((*x.shape[:-1], -(-cols // 128)), dtype=torch.float32, device=x.device)
         _mm._check(_mm.lib().mega_moe_quantize_rows(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, cols,
                                                     _logit_kinds()[x.dtype], raw), "quantize_rows")
@@ -652,7 +652,7 @@ def dequantize_rows(codes, scales, dtype=None, stream=None):
     if cols >> 31:
         _int32(cols=cols)
     with _Call(codes.device, stream, codes, scales) as raw:
-        y = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+        y = torch.empty_like(codes, dtype=dtype)
         _mm._check(_mm.lib().mega_moe_dequantize_rows(codes.data_ptr(), scales.data_ptr(), y.data_ptr(), codes.numel() // cols,
                                                       cols, kinds[dtype], raw), "dequantize_rows")
     return _unrecorded("dequantize_rows", "the rounding to 8 bits has none", y, scales)
@@ -679,11 +679,12 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False, dtype=None, str
     if residual is not None:
         _want("residual", residual, x.shape, (x.dtype, torch.float32), device)
     with _Call(device, stream, x, weight, residual) as raw:
-        h = None if residual is None else torch.empty(x.shape, dtype=residual.dtype, device=device)
-        y = torch.empty(x.shape, dtype=dtype, device=device) if quantize is not True else None
+        # (empty_like takes half of empty's host time)
+        h = None if residual is None else torch.empty_like(residual)
+        y = None if quantize is True else torch.empty_like(x) if dtype is x.dtype else torch.empty_like(x, dtype=dtype)
         codes = scales = None
         if quantize:
-            codes = torch.empty(x.shape, dtype=torch.uint8, device=device)
+            codes = torch.empty_like(x, dtype=torch.uint8)
             scales = torch.empty((*x.shape[:-1], -(-hidden // 128)), dtype=torch.float32, device=device)
         # a stream as it stands goes in as the residual, which may have another type than y
         first, second = (x, residual) if residual is not None or x.dtype == dtype else (None, x)
@@ -724,7 +725,7 @@ def rms_norm_backward(dy, h, weight, eps=1e-6, dresidual=None, stream=None):
         _want("dresidual", dresidual, dy.shape, (kind,) if scales is None else (dy.dtype, torch.float32), device)
     nbytes = _norm_bytes(rows, hidden)
     with _Call(device, stream, dy, values, scales, weight, dresidual) as raw:
-        dx = torch.empty(dy.shape, dtype=kind, device=device)
+        dx = torch.empty_like(dy) if kind is dy.dtype else torch.empty_like(dy, dtype=kind)
         dweight = torch.empty(hidden, dtype=torch.float32, device=device)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
         _mm._check(_mm.lib().mega_moe_rms_norm_backward(
@@ -771,7 +772,7 @@ def swiglu(gate_up, checkpoint=False, offsets=None, status=None, stream=None):
         act = torch.empty((rows, inter), dtype=gate_up.dtype, device=device)
         codes = scales = None
         if checkpoint:
-            codes = torch.empty(gate_up.shape, dtype=torch.uint8, device=device)
+            codes = torch.empty_like(gate_up, dtype=torch.uint8)
             scales = torch.empty((rows, 2 * -(-inter // 128)), dtype=torch.float32, device=device)
         _mm._check(_mm.lib().mega_moe_swiglu(gate_up.data_ptr(), act.data_ptr(), _at(codes), _at(scales), _at(offsets), groups,
                                              rows, inter, kinds[gate_up.dtype], _at(status), raw), "swiglu")
@@ -799,7 +800,7 @@ def swiglu_backward(dact, gate_up, recompute=False, offsets=None, status=None, s
     groups = _swiglu_groups(offsets, status, device)
     with _Call(device, stream, dact, values, scales, offsets, status) as raw:
         dgate_up = torch.empty((rows, 2 * inter), dtype=dact.dtype, device=device)
-        act = torch.empty((rows, inter), dtype=dact.dtype, device=device) if recompute else None
+        act = torch.empty_like(dact) if recompute else None
         _mm._check(_mm.lib().mega_moe_swiglu_backward(
             dact.data_ptr(), values.data_ptr(), _at(scales), dgate_up.data_ptr(), _at(act), _at(offsets), groups, rows, inter,
             kinds[dact.dtype], _at(status), raw), "swiglu_backward")
