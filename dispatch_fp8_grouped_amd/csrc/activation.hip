@@ -50,13 +50,6 @@ __global__ __launch_bounds__(256) void quantize_kernel(const void* x, uint8_t* c
     }
 }
 
-// In fp16 the rounding to four bits takes 65504 and its neighbours to 65536, which fp16 does not have: they come back as 65504.
-template <class T>
-__device__ __forceinline__ float restored(float v) {
-    if constexpr (T::kNarrow) return fabsf(v) == 65536.0f ? copysignf(65504.0f, v) : v;
-    else return v;
-}
-
 template <class T>
 __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, const float* scales, void* y, int rows, int cols) {
     for (Walk w(scale_blocks(cols), 0); w.row < rows; w.next()) {
@@ -68,16 +61,6 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint8_t* codes, c
         Row8<T>::store(y, (size_t)w.row * cols + c, cols - c, v);
     }
 }
-template <>
-__global__ __launch_bounds__(256) void dequantize_kernel<Fp32>(const uint8_t* codes, const float* scales, void* y, int rows, int cols) {
-    for (Walk w(scale_blocks(cols), 0); w.row < rows; w.next()) {
-        const int c = w.block * kScaleCols + (threadIdx.x & 15) * 8;
-        float v[8];
-        Codes8::load<false>(codes, (size_t)w.row * cols + c, cols - c).get(scales[(size_t)w.row * w.blocks + w.block], v);
-        Row8<Fp32>::store(y, (size_t)w.row * cols + c, cols - c, v);
-    }
-}
-
 struct SwigluArgs {
     const void *dact, *gate_up;     // gate_up: values, or codes (backward)
     const float* in_scales;         // of codes
@@ -199,15 +182,6 @@ int32_t check_swiglu(const SwigluArgs& a, int64_t rows, int32_t dtype) {
 }
 
 }  // namespace
-
-hipError_t launch_dequantize(const uint8_t* codes, const float* scales, void* y, int rows, int cols, int dtype, hipStream_t st) {
-    const dim3 grid = walk_grid(rows, cols);
-    if (dtype == MEGA_MOE_BF16) hipLaunchKernelGGL((dequantize_kernel<Bf16>), grid, dim3(256), 0, st, codes, scales, y, rows, cols);
-    else if (dtype == MEGA_MOE_FP16) hipLaunchKernelGGL((dequantize_kernel<Fp16>), grid, dim3(256), 0, st, codes, scales, y, rows, cols);
-    else hipLaunchKernelGGL((dequantize_kernel<Fp32>), grid, dim3(256), 0, st, codes, scales, y, rows, cols);
-    return hipGetLastError();
-}
-
 }  // namespace mm
 
 using namespace mm;
@@ -231,8 +205,12 @@ int32_t mega_moe_dequantize_rows(const uint8_t* codes, const float* scales, void
     if (!rows_supported(rows, cols) || (!half(dtype) && dtype != MEGA_MOE_FP32)) return MEGA_MOE_ERR_UNSUPPORTED;
     if (rows == 0) return MEGA_MOE_OK;
     if (!element(y, dtype) || !codes || !word(scales)) return MEGA_MOE_ERR_INVALID_ARG;
-    return launch_dequantize(codes, scales, y, (int)rows, cols, dtype, static_cast<hipStream_t>(stream)) == hipSuccess ? MEGA_MOE_OK
-                                                                                                                     : MEGA_MOE_ERR_HIP;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const dim3 grid = walk_grid(rows, cols);
+    if (dtype == MEGA_MOE_BF16) hipLaunchKernelGGL((dequantize_kernel<Bf16>), grid, dim3(256), 0, st, codes, scales, y, (int)rows, cols);
+    else if (dtype == MEGA_MOE_FP16) hipLaunchKernelGGL((dequantize_kernel<Fp16>), grid, dim3(256), 0, st, codes, scales, y, (int)rows, cols);
+    else hipLaunchKernelGGL((dequantize_kernel<Fp32>), grid, dim3(256), 0, st, codes, scales, y, (int)rows, cols);
+    return hipGetLastError() == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
 int32_t mega_moe_swiglu(const void* gate_up, void* act, uint8_t* codes, float* scales, const int32_t* offsets, int32_t groups,

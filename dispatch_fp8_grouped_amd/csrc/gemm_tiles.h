@@ -61,6 +61,14 @@ struct Fp16 {
     static __device__ __forceinline__ float high(uint32_t w) { return (float)__builtin_bit_cast(f16x2_t, w)[1]; }
 };
 
+// A value of 8-bit rows before it becomes a T.  Rounding to four bits takes fp16's largest numbers to 65536, which fp16 does
+// not have: they come back as 65504.
+template <class T>
+__device__ __forceinline__ float restored(float v) {
+    if constexpr (T::kNarrow) return fabsf(v) == 65536.0f ? copysignf(65504.0f, v) : v;
+    else return v;
+}
+
 constexpr int kStepK = 64;                   // contraction values per step: 128 bytes of a KC row
 constexpr uint32_t kPastEnd = 0x80000000u;   // an offset that no descriptor here reaches (num_records < 2^31)
 

@@ -14,12 +14,10 @@
 // 16384 rows, 32 x 4096 x 7168, fp32, 1.39 ms for 962 GFLOP and 4.1 GB.
 #include <type_traits>
 
+#include "codes_loop.h"
 #include "gemm_kernels.h"
 
 namespace mm {
-
-hipError_t launch_dequantize(const uint8_t* codes, const float* scales, void* y, int rows, int cols, int dtype, hipStream_t st);
-
 namespace {
 
 struct GroupedArgs {
@@ -184,6 +182,60 @@ __global__ __launch_bounds__(512) void grouped_weight_stream_kernel(GroupedArgs 
     });
 }
 
+// backward_weight from 8-bit rows: one 256 x 128 tile of dw[e] per work-group, tiles to XCDs as above.  The launch is no
+// stream of tiles: a work-group that ends leaves its stores on their way and its place on the CU to the next one.
+struct CodesArgs {
+    GroupedArgs g;               // p: dy
+    const uint8_t* codes;
+    const float* scales;
+};
+template <class T, bool kFp32>
+__global__ __launch_bounds__(256, 2) void grouped_codes_kernel(CodesArgs c) {
+    using L = CodesLoop<T>;
+    const GroupedArgs& a = c.g;
+    __shared__ __align__(1024) uint8_t smem[L::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ntm = (a.n + L::BM - 1) / L::BM, ntq = (a.k + L::BN - 1) / L::BN;
+    const int per = (ntm * ntq + 7) >> 3, part = (int)((blockIdx.x >> 3) % a.parts), b = (int)((blockIdx.x >> 3) / a.parts), nth = b / per,
+              li = (blockIdx.x & 7) * per + b - nth * per;
+    if (nth >= a.groups || li >= ntm * ntq) return;
+    const int g = a.groups <= 64 ? group_by_length(a.off, a.groups, a.rows, nth, lane) : nth;
+    const int band = li / (4 * ntq), in = li - band * 4 * ntq, width = min(4, ntm - band * 4);
+    const int qt = in / width, m0 = (band * 4 + in - qt * width) * L::BM, q0 = qt * L::BN;
+    int lo, cnt;
+    bool bad = false;
+    group_rows(a.off, g, a.rows, lo, cnt, bad);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    cnt = __builtin_amdgcn_readfirstlane(cnt);
+    if (bad && li == 0 && threadIdx.x == 0 && a.status) atomicOr(a.status, MEGA_MOE_STATUS_BAD_LAYOUT);
+    if (cnt == 0 && a.accumulate && a.parts == 1) return;
+    if (a.parts > 1) {
+        const int share = ((cnt + L::kDepth - 1) / L::kDepth + a.parts - 1) / a.parts * L::kDepth, from = min(part * share, cnt);
+        lo += from;
+        cnt = min(cnt - from, share);
+    }
+    const int blocks = (a.k + 127) / 128;
+    typename L::Acc acc[L::QI][L::MI];
+    const uint16_t* p = a.p + (size_t)lo * a.n;
+    const uint8_t* x = c.codes + (size_t)lo * a.k;
+    const float* scales = c.scales + (size_t)lo * blocks;
+    L::run(p, a.n, m0, x, a.k, q0, scales, blocks, cnt, smem, wave, lane, acc);
+    const size_t at = (((size_t)part * a.groups + g) * a.n + m0) * a.k + q0;
+    if constexpr (kFp32) {
+        float* out = static_cast<float*>(a.out) + at;
+        store_tile<L, 4>(
+            acc, smem, a.n - m0, a.k - q0, wave, lane, [](uint8_t* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; },
+            [&](int m, int col, i32x4 v) {
+                f32x4* o = reinterpret_cast<f32x4*>(out + (size_t)m * a.k + col);
+                f32x4 sum = __builtin_bit_cast(f32x4, v);
+                if (a.accumulate) sum += *o;
+                *o = sum;
+            });
+    } else {
+        store_halves<L, T>(acc, static_cast<uint16_t*>(a.out) + at, a.n - m0, a.k - q0, a.k, smem, wave, lane);
+    }
+}
+
 // dw = the parts added up in their order (dw += with accumulate); values is a multiple of 8
 template <class T, bool kFp32>
 __global__ __launch_bounds__(256) void grouped_join_kernel(const float* parts, int n_parts, size_t values, void* out,
@@ -307,6 +359,46 @@ hipError_t launch_weight(GroupedArgs a, void* workspace, hipStream_t st) {
     return hipGetLastError();
 }
 
+// From 8-bit rows.  Where the output has many 256 x 256 tiles for every CU, the rows are restored first and take the 16-bit
+// product, whose large tiles need fewer loads for each MFMA; below that the codes are read by the product itself, and no
+// 16-bit copy is made.  Restored and read as codes, bf16: 32 groups of 1024 rows, 4096 x 7168, 1881 and 1920 us; 32 of 128,
+// 7168 x 2048, 225 and 301; 32 of 1024, 4096 x 1536, 428 and 412; 8 of 1024, 2048 x 2048, 79 and 68; 10 of 200, 1000 x 2056, 32 and
+// 23; one of 4096, 1024 x 2048, 34 and 33.  (Rows shorter than the loads of 16 codes are restored too.)
+constexpr int kCodesLarge = 2048;
+bool codes_restored(int n, int k, int groups) { return k < 16 || weight_tiles(n, k, groups, 256) >= kCodesLarge; }
+// 256 x 128 tiles, two to a CU; where these leave CUs without work and the groups are long, the rows are split into parts of
+// at least 512 (of an average group), as many as give every CU one tile: what the second launch adds up grows with them (4096
+// rows, 1024 x 2048: 33 us with one tile to a CU, 41 with two, 45 with half of one).
+int64_t codes_tiles(int n, int k, int groups) { return (int64_t)groups * ((n + 255) / 256) * ((k + 127) / 128); }
+int codes_parts(int64_t rows, int n, int k, int groups) {
+    const int64_t by_tiles = 256 / codes_tiles(n, k, groups), by_rows = rows / groups / 512;
+    const int64_t parts = by_tiles < by_rows ? by_tiles : by_rows;
+    return (int)(parts < 1 ? 1 : parts);
+}
+
+template <class T, bool kFp32>
+hipError_t launch_codes_tiles(const CodesArgs& a, hipStream_t st) {
+    const int64_t tiles = codes_tiles(a.g.n, a.g.k, 1);
+    hipLaunchKernelGGL((grouped_codes_kernel<T, kFp32>), dim3((uint32_t)((tiles + 7) / 8 * 8 * a.g.groups * a.g.parts)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
+template <class T, bool kFp32>
+hipError_t launch_codes(CodesArgs a, void* workspace, hipStream_t st) {
+    if (a.g.parts == 1) return launch_codes_tiles<T, kFp32>(a, st);
+    void* dw = a.g.out;
+    const int accumulate = a.g.accumulate;
+    a.g.out = workspace;
+    a.g.accumulate = 0;
+    const hipError_t e = launch_codes_tiles<T, true>(a, st);
+    if (e != hipSuccess) return e;
+    const size_t values = (size_t)a.g.groups * a.g.n * a.g.k;
+    const size_t blocks = (values + 1023) / 1024;
+    hipLaunchKernelGGL((grouped_join_kernel<T, kFp32>), dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st,
+                       static_cast<const float*>(workspace), a.g.parts, values, dw, accumulate);
+    return hipGetLastError();
+}
+
 // a launch has fewer than 2^32 threads: at most 2^22 tiles of any shape
 bool too_many_tiles(int64_t rows, int cols, int groups) {
     return (rows / 128 + groups) * ((cols + 127) / 128) > (int64_t)1 << 22;
@@ -380,28 +472,53 @@ int32_t mega_moe_grouped_backward_weight(const void* dy, const void* x, const in
     return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
-// Rows kept in 8 bits: restored behind the parts of the sum, then the product above.
 int32_t mega_moe_grouped_codes_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t groups, uint64_t* bytes_out) {
-    const int32_t rc = mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups, bytes_out);
-    if (rc == MEGA_MOE_OK) *bytes_out += (uint64_t)rows * k * 2;
-    return rc;
+    if (!bytes_out || rows < 0 || n < 0 || k < 0 || groups < 0) return MEGA_MOE_ERR_INVALID_ARG;
+    if (!sizes_supported(rows, n, k, groups)) return MEGA_MOE_ERR_UNSUPPORTED;
+    if (codes_restored(n, k, groups)) {
+        const int32_t rc = mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups, bytes_out);
+        *bytes_out += (uint64_t)rows * k * 2;
+        return rc;
+    }
+    const int parts = codes_parts(rows, n, k, groups);
+    *bytes_out = parts > 1 ? (uint64_t)parts * groups * n * k * 4 : 0;
+    return MEGA_MOE_OK;
 }
 
 int32_t mega_moe_grouped_backward_weight_codes(const void* dy, const uint8_t* codes, const float* scales, const int32_t* offsets,
                                                void* dw, int64_t rows, int32_t n, int32_t k, int32_t groups, int32_t dtype,
                                                int32_t out_dtype, int32_t accumulate, void* workspace, uint64_t workspace_bytes,
                                                uint32_t* device_status, void* stream) {
-    const int32_t rc = check_grouped(dy, workspace, offsets, dw, rows, n, k, groups, dtype, device_status, true);
+    const int32_t rc = check_grouped(dy, dy, offsets, dw, rows, n, k, groups, dtype, device_status, true);
     if (rc) return rc;
-    if (rows > 0 && (!codes || !scales || ((uintptr_t)scales & 3u))) return MEGA_MOE_ERR_INVALID_ARG;
-    uint64_t need = 0;
-    mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups, &need);
-    if (workspace_bytes < need + (uint64_t)rows * k * 2) return MEGA_MOE_ERR_WORKSPACE_TOO_SMALL;
-    void* x = static_cast<char*>(workspace) + need;
-    if (rows > 0 && launch_dequantize(codes, scales, x, (int)rows, k, dtype, static_cast<hipStream_t>(stream)) != hipSuccess)
-        return MEGA_MOE_ERR_HIP;
-    return mega_moe_grouped_backward_weight(dy, x, offsets, dw, rows, n, k, groups, dtype, out_dtype, accumulate, workspace, need,
-                                            device_status, stream);
+    if (out_dtype != dtype && out_dtype != MEGA_MOE_FP32) return MEGA_MOE_ERR_UNSUPPORTED;
+    if (accumulate && out_dtype != MEGA_MOE_FP32) return MEGA_MOE_ERR_UNSUPPORTED;
+    if (weight_tiles(n, k, groups, 256) > (int64_t)1 << 21) return MEGA_MOE_ERR_UNSUPPORTED;
+    if (rows > 0 && (!codes || ((uintptr_t)codes & 7u) || !scales || ((uintptr_t)scales & 3u))) return MEGA_MOE_ERR_INVALID_ARG;
+    if (codes_restored(n, k, groups)) {       // restored behind the parts of the sum, then the product of 16-bit rows
+        uint64_t need = 0;
+        mega_moe_grouped_weight_workspace_bytes(rows, n, k, groups, &need);
+        if (rows > 0 && !aligned16(workspace)) return MEGA_MOE_ERR_INVALID_ARG;
+        if (workspace_bytes < need + (uint64_t)rows * k * 2) return MEGA_MOE_ERR_WORKSPACE_TOO_SMALL;
+        void* x = static_cast<char*>(workspace) + need;
+        if (mega_moe_dequantize_rows(codes, scales, x, rows, k, dtype, stream) != MEGA_MOE_OK) return MEGA_MOE_ERR_HIP;
+        return mega_moe_grouped_backward_weight(dy, x, offsets, dw, rows, n, k, groups, dtype, out_dtype, accumulate, workspace, need,
+                                                device_status, stream);
+    }
+    const int parts = codes_parts(rows, n, k, groups);
+    if (parts > 1) {
+        if (!aligned16(workspace)) return MEGA_MOE_ERR_INVALID_ARG;
+        if (workspace_bytes < (uint64_t)parts * groups * n * k * 4) return MEGA_MOE_ERR_WORKSPACE_TOO_SMALL;
+    }
+    const CodesArgs a{{static_cast<const uint16_t*>(dy), nullptr, dw, offsets, device_status, (int)rows, n, k, groups, accumulate != 0, parts},
+                      codes, scales};
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (out_dtype == MEGA_MOE_FP32)
+        e = dtype == MEGA_MOE_BF16 ? launch_codes<Bf16, true>(a, workspace, st) : launch_codes<Fp16, true>(a, workspace, st);
+    else
+        e = dtype == MEGA_MOE_BF16 ? launch_codes<Bf16, false>(a, workspace, st) : launch_codes<Fp16, false>(a, workspace, st);
+    return e == hipSuccess ? MEGA_MOE_OK : MEGA_MOE_ERR_HIP;
 }
 
 }  // extern "C"

@@ -16,7 +16,9 @@
 
 namespace mm {
 
-struct Fp32 {};
+struct Fp32 {
+    static constexpr bool kNarrow = false;
+};
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));      // 16 bytes at an address of 2-byte alignment
 typedef u32x4 u32x4_any4 __attribute__((aligned(4)));

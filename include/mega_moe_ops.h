@@ -185,9 +185,10 @@ int32_t mega_moe_dequantize_rows(const uint8_t* codes, const float* scales, void
  *   dw[e] = sum over the rows m of group e of dy[m]^T x[m],   x[m] = codes * scales
  *   dy dtype [rows][n], codes uint8 [rows][k], scales float [rows][ceil(k / 128)].  A value enters the product in dtype:
  *   exactly with scales that are powers of two, unless it leaves fp16's range (as in dequantize_rows), else rounded.
- * Everything else, the limits and errors included, as for mega_moe_grouped_backward_weight, but codes and scales need not be
- * aligned beyond their type, and
- *   workspace  mega_moe_grouped_codes_workspace_bytes() bytes */
+ * Everything else, the limits and errors included, as for mega_moe_grouped_backward_weight, but codes are 8-byte and scales
+ * 4-byte aligned, codes and scales of rows of no group may be read (and count for nothing), and
+ *   workspace  mega_moe_grouped_codes_workspace_bytes() bytes: for the parts of a split sum, and with many tiles of dw for
+ *              the rows in 16 bits */
 int32_t mega_moe_grouped_codes_workspace_bytes(int64_t rows, int32_t n, int32_t k, int32_t groups, uint64_t* bytes_out /* host */);
 int32_t mega_moe_grouped_backward_weight_codes(const void* dy, const uint8_t* codes, const float* scales, const int32_t* offsets,
                                                void* dw, int64_t rows, int32_t n, int32_t k, int32_t groups, int32_t dtype,

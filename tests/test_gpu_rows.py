@@ -331,7 +331,9 @@ def test_swiglu_takes_the_rows_of_the_groups_alone():
 WEIGHTS = [([1], 8, 8), ([0, 1, 0], 64, 72), ([3, 0, 17, 16, 15, 1], 264, 520), ([127, 128, 129, 1], 256, 192), ([700, 0, 0, 900], 768, 1096),
            ([2048], 512, 64), ([1] * 100 + [0] * 50 + [7] * 50, 72, 128), ([40] * 8, 2056, 2048), ([3000, 0, 2500, 1300, 257], 4104, 200),
            ([3000, 17, 0, 900], 4104, 2056), ([64], 2056, 7168), ([20000], 72, 64), ([9000, 0, 3, 4000], 136, 264),
-           ([63, 64, 65, 0, 1, 2, 129], 2048, 2184)]
+           ([63, 64, 65, 0, 1, 2, 129], 2048, 2184), ([5000, 0, 3], 64, 8), ([31, 32, 33, 95, 96, 97], 264, 24),
+           # so many tiles that the rows are restored first
+           ([40, 0, 25], 8200, 8200)]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
@@ -455,3 +457,28 @@ def test_more_than_32_bits_of_values_in_a_norm():
     ref.close(dx[-3:], want, 192 * U * size, "dx")
     del x, y, dx
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("powers", [True, False])
+def test_weight_gradient_takes_the_restored_values(kind, powers):
+    """With dy the identity dw is x itself: every code under scales of all sizes, as dequantize_rows restores it."""
+    rows, k = 256, 520
+    g = gen(11)
+    codes = torch.randint(0, 256, (rows, k), generator=g, device="cuda").to(torch.uint8)
+    codes[(codes & 127) == 127] = 0                    # NaN would meet dy's zeros in every row
+    codes[:, :256] = torch.arange(256, device="cuda").to(torch.uint8)
+    codes[:, 127] = codes[:, 255] = 0
+    low, high = (-110, 118) if kind == "bf16" else (-30, 7)
+    scales = torch.exp2(torch.randint(low, high + 1, (rows, 5), generator=g, device="cuda").float())
+    if not powers:
+        scales = scales * (1 + torch.rand(rows, 5, generator=g, device="cuda") * 0.75)
+    if kind == "fp16" and powers:                      # 256 * 2^8 comes back as 65504
+        scales[3, 4], codes[3, 512:] = 256.0, 0x78
+    dy = torch.eye(rows, device="cuda", dtype=KINDS[kind])
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    want = mm.dequantize_rows(codes, scales, dtype=KINDS[kind])
+    dw = mm.grouped_backward_weight(dy, (codes, scales), off, dtype=FP32)
+    fine = torch.isfinite(want).all(0)                 # beyond fp16's range an infinity meets dy's zeros in its column
+    assert fine.all() or (kind == "fp16" and not powers and fine.sum() > 100)
+    assert torch.equal(dw[0][:, fine], want.float()[:, fine])
