@@ -321,8 +321,12 @@ __device__ __forceinline__ void store_halves(const typename L::Acc (&acc)[L::QI]
 // order, so the fourth wait, one and a half steps (2 us) into the next tile, is for all of the stores; a CU's share of
 // the fill rate takes about 10 us for a tile's 256 KB of fp32.  Their issue has no MFMA beside it.
 //
+// kLines: the output's rows are whole lines of 128 bytes, which the stores then send past the caches (16384 rows, skewed,
+// 32 x 7168 x 2048, fp32: 643 -> 611 us; 32768 rows, 32 x 4096 x 7168, bf16: 1795 -> 1776).  Lines that two tiles share must meet
+// in a cache.
+//
 // Tiles: next() gives the stream's next tile, made by of(); one without steps is its end.
-template <class T, int kBytes>
+template <class T, int kBytes, bool kLines>
 struct KsStream {
     static constexpr int BM = 256, BN = 256;
     using L = QuadLoop<T, true, true, BM, BN, 4, 2>;
@@ -392,7 +396,7 @@ struct KsStream {
                     const bool exists = m < t.rows && c < t.cols;
                     const uint32_t off = exists ? (uint32_t)m * ldb + (uint32_t)c * kBytes : kPastEnd;
                     v = change(t.out + off, exists, v);
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), desc, (int)off, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), desc, (int)off, 0, kLines ? 2 : 0);   // 2: nt
                 }
                 __builtin_amdgcn_wave_barrier();
             }

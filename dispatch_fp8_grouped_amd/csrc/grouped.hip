@@ -127,10 +127,10 @@ __global__ __launch_bounds__(L::kThreads) void grouped_weight_kernel(GroupedArgs
 // backward_weight with enough large tiles for every CU: a stream of them per work-group, 32 work-groups to an XCD.
 // Each XCD takes an eighth of every group's tiles, longest group first, and its work-groups take turns.
 constexpr int kStreams = 32;
-template <class T, bool kFp32>
+template <class T, bool kFp32, bool kLines>
 __global__ __launch_bounds__(512) void grouped_weight_stream_kernel(GroupedArgs a) {
     constexpr int kBytes = kFp32 ? 4 : 2;
-    using S = KsStream<T, kBytes>;
+    using S = KsStream<T, kBytes, kLines>;
     static_assert(S::kThreads == 512, "one launch");
     __shared__ __align__(1024) uint8_t smem[S::kLds];
     // the groups in the order of their tiles: longest first where 64 lanes can rank them (long and short ones in turn,
@@ -342,7 +342,10 @@ hipError_t launch_small_weight(const GroupedArgs& a, hipStream_t st) {
 template <class T, bool kFp32>
 hipError_t launch_weight(GroupedArgs a, void* workspace, hipStream_t st) {
     if (weight_tiles(a.n, a.k, a.groups, 256) >= kWeightLarge) {
-        hipLaunchKernelGGL((grouped_weight_stream_kernel<T, kFp32>), dim3(8 * kStreams), dim3(512), 0, st, a);
+        if ((uint32_t)a.k * (kFp32 ? 4u : 2u) % 128 == 0 && ((uintptr_t)a.out & 127u) == 0)
+            hipLaunchKernelGGL((grouped_weight_stream_kernel<T, kFp32, true>), dim3(8 * kStreams), dim3(512), 0, st, a);
+        else
+            hipLaunchKernelGGL((grouped_weight_stream_kernel<T, kFp32, false>), dim3(8 * kStreams), dim3(512), 0, st, a);
         return hipGetLastError();
     }
     if (a.parts == 1) return launch_small_weight<T, kFp32>(a, st);
