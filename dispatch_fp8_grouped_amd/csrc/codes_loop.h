@@ -12,6 +12,11 @@
 //   starts the loads of P for step s + 2 and of the codes for step s + 3,
 //   reads its codes of step s + 1, which it loaded itself, and writes them as 16-bit numbers to the other one of X's two stages.
 // So a load has two steps to arrive.  Rows behind the group's end are zeros in both operands and are not read.
+//
+// Measured, bf16: 2000 rows in 10 groups, 1000 x 2056, 24 us, and 28 for the product of the same rows in 16 bits; 8 groups of 1024,
+// 2048 x 2048, 72 and 70; one group of 16384, 4096 x 4096, 470 (1170 TFLOP/s) and 430.  Many steps over many tiles are bound by the loads'
+// latency beside the MFMAs: of 1995 us (32 groups of 1024, 4096 x 7168), 1390 remain without loads, 1725 with loads that meet L2,
+// 1745 without the conversion.
 #pragma once
 
 #include "gemm_kernels.h"

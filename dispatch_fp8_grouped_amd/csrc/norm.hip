@@ -3,7 +3,12 @@
 //   forward    v = x + residual, r = 1 / sqrt(mean v^2 + eps), y = v r w
 //   backward   r as above from h, n = h r, g = dy w:  dx = r (g - n mean(g n)) + dresidual,  dw = sum over rows of dy n
 // One pass over memory: a row stays in the registers of its lanes between its reduction and its outputs.  All arithmetic
-// is fp32; y and the codes come from the unrounded sum v, each with its one rounding.
+// is fp32 but the sums over a row, which are joined in fp64; y and the codes come from the unrounded sum v, each with its
+// one rounding.
+//
+// Bound by memory.  Measured, bf16, 32768 x 7168: x, residual, h, y and codes 360 us (2.12 GB, 5.9 TB/s); x and y 193 us
+// (4.9); the gradient with dresidual 354 us (1.88 GB, 5.3).  1024 x 7168 from an fp32 stream to codes: 17 us (4.8).  One row: 3.5 us,
+// of which the launch is most.
 #include <type_traits>
 
 #include "row_io.h"
@@ -56,6 +61,14 @@ __device__ __forceinline__ double inverse_root(double a) {
     return a > 0.0 && a < __builtin_inf() ? r * (1.5 - 0.5 * a * r * r) : r;
 }
 
+// y + rest, |rest| at most half a step of y, as y or, where y is even and there is a rest, the odd neighbour on its side:
+// rounding it to fewer bits rounds y + rest.
+__device__ __forceinline__ float odd(float y, float rest) {
+    const uint32_t b = __float_as_uint(y);
+    const uint32_t step = (int)(__float_as_uint(rest) ^ b) < 0 ? ~0u : 1u;
+    return rest != 0.0f && !(b & 1u) && y != 0.0f ? __uint_as_float(b + step) : y;
+}
+
 // Where a lane stands: its row within the work-group, its place among the row's lanes, and their number.
 template <int kLanes>
 struct Place {
@@ -68,8 +81,9 @@ struct Place {
     }
 };
 
-// T: x, y (and weight); R: residual, h.  A row's units of 8 columns go to its lanes in turn, kUnits to each.
-template <class T, class R, int kLanes, int kUnits>
+// T: x, y (and weight); R: residual, h.  A row's units of 8 columns go to its lanes in turn, kUnits to each.  kCodes: y in 8
+// bits as well, or alone.
+template <class T, class R, bool kCodes, int kLanes, int kUnits>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs a) {
     __shared__ double lds[32][1];
     const Place<kLanes> p;
@@ -100,8 +114,6 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
         }
         double sum[1] = {squares};
         row_sums<kLanes>(sum, lds, turn);
-        // y = v (r w) with what r and r w lose added to the product: within half a step of fp32 of v r w.  The number of values
-        // that fall on the other side of an 8-bit border is proportional to that error, and the pass takes as long (353 us).
         const double root = inverse_root(sum[0] * a.mean + a.eps);
         const float r = (float)root, lost = root < __builtin_inf() ? (float)(root - (double)r) : 0.f;
 #pragma unroll
@@ -109,14 +121,27 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
             const int c = (u * p.lanes + p.lane) * 8, n = a.hidden - c;
             float w[8];
             weights8<T>(a.weight, a.weight_fp32, c, n, w);
+            if constexpr (!kCodes) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float rw = r * w[i], less = __builtin_fmaf(lost, w[i], __builtin_fmaf(r, w[i], -rw));
-                v[u][i] = __builtin_fmaf(v[u][i], rw, v[u][i] * less);
-            }
-            if (a.y) Row8<T>::store(a.y, at + c, n, v[u]);
-            if (a.codes) {
+                for (int i = 0; i < 8; ++i) v[u][i] *= r * w[i];
+                if (a.y) Row8<T>::store(a.y, at + c, n, v[u]);
+            } else {
+                // For the codes what the products lose is added to them: y is within half a step of fp32 of v r w, and what is
+                // left of it makes y odd, which the halves between two codes are not.  So the codes are those of v r w but
+                // for r's last bit and v's rounding: of 44 million values 4 fell on the other side of a half, 20 with fp32 products
+                // alone (32768 x 7168, y and codes: 360 us against 353).
+                float rest[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float rw = r * w[i], less = v[u][i] * __builtin_fmaf(lost, w[i], __builtin_fmaf(r, w[i], -rw));
+                    const float y = __builtin_fmaf(v[u][i], rw, less);
+                    rest[i] = __builtin_fmaf(v[u][i], rw, -y) + less;
+                    v[u][i] = y;
+                }
+                if (a.y) Row8<T>::store(a.y, at + c, n, v[u]);
                 const Scale s(max16(largest(v[u])));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[u][i] = odd(v[u][i], rest[i]);
                 s.template store<true>(a.codes, at + c, n, v[u]);
                 if ((p.lane & 15) == 0 && n > 0) a.scales[(size_t)row * scale_blocks(a.hidden) + c / kScaleCols] = s.scale;
             }
@@ -300,8 +325,9 @@ int grad_blocks(int64_t rows, int hidden) {
 template <class T, class R, int kLanes, int kUnits>
 hipError_t launch_norm_with(const NormArgs& a, const RowShape8& s, hipStream_t st) {
     const int64_t blocks = ((int64_t)a.rows + s.rows - 1) / s.rows;
-    hipLaunchKernelGGL((rms_norm_kernel<T, R, kLanes, kUnits>), dim3((uint32_t)(blocks < (1 << 20) ? blocks : 1 << 20)),
-                       dim3(s.threads), 0, st, a);
+    const dim3 grid((uint32_t)(blocks < (1 << 20) ? blocks : 1 << 20)), threads(s.threads);
+    if (a.codes) hipLaunchKernelGGL((rms_norm_kernel<T, R, true, kLanes, kUnits>), grid, threads, 0, st, a);
+    else hipLaunchKernelGGL((rms_norm_kernel<T, R, false, kLanes, kUnits>), grid, threads, 0, st, a);
     return hipGetLastError();
 }
 template <class T, class R>

@@ -235,10 +235,11 @@ struct Scale {
     }
 };
 
-// Whether a pass reads more than the last-level cache holds (256 MB): what it reads is then in no cache, and is read past
-// them.  Measured past them and not: 32768 rows, quantize of 7168 columns 119 and 132 us, the norm's gradient 354 and
-// 362, SwiGLU of 2048 with its input kept 85 and 90; 4096 rows, read while they are in the cache: 17.6 and 15.7, 48 and 42, 14 and 12.
-inline bool beyond_cache(uint64_t bytes) { return bytes > (uint64_t)256 << 20; }
+// Whether a pass reads more than three quarters of the last-level cache (256 MB), which its outputs share: most of what it
+// reads is then in no cache, and is read past them.  Measured past them and not: 32768 rows, quantize of 7168 columns 119 and 132 us,
+// the norm's gradient 354 and 362, SwiGLU of 2048 with its input kept 85 and 100; 16384 rows of 7168 columns (235 MB), quantize, 61
+// and 67, 12288 rows 47 and 45; 4096 rows 17.6 and 15.7, the norm's gradient 48 and 42, SwiGLU 14 and 12.
+inline bool beyond_cache(uint64_t bytes) { return bytes > (uint64_t)192 << 20; }
 
 constexpr int kScaleCols = 128;      // columns of one scale
 __host__ __device__ inline int scale_blocks(int cols) { return (cols + kScaleCols - 1) / kScaleCols; }

@@ -18,8 +18,8 @@ devices, allocate what they return, and call them.  Everything runs in the HIP k
     dx, dweight = mm.rms_norm_backward(dy, h, weight, dresidual=dh)
 
 Tensors must be dense, on one GPU; a slice of tokens that the router or the ordering is given may start anywhere, so may
-the rows of the norm, of SwiGLU and in 8 bits, and the other tensors start at a multiple of 16 bytes, as slices of their
-rows do; `out` and `workspace` share no memory with the other tensors.  Calls run on the current
+the rows of the norm, of SwiGLU and in 8 bits (in the grouped products: at a multiple of 8 bytes), and the other tensors
+start at a multiple of 16 bytes, as slices of their rows do; `out` and `workspace` share no memory with the other tensors.  Calls run on the current
 stream of that GPU, or on `stream` (a torch stream or a stream handle); a tensor that a call returns belongs to the
 stream of the call.  The tensors given with `stream` are recorded on it, so that their memory is not handed out
 again before the call has read it; that they are ready by then is up to the caller, as for any stream.
@@ -634,7 +634,7 @@ def quantize_rows(x, stream=None):
     rows, cols = _rows("x", x)
     with _Call(x.device, stream, x) as raw:
         codes = torch.empty_like(x, dtype=torch.uint8)
-        scales = torch.empty((*x.shape[:-1], -(-cols // 128)), dtype=torch.float32, device=x.device)
+        scales = x.new_empty((*x.shape[:-1], -(-cols // 128)), dtype=torch.float32)
         _mm._check(_mm.lib().mega_moe_quantize_rows(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, cols,
                                                     _logit_kinds()[x.dtype], raw), "quantize_rows")
     return codes, scales
@@ -679,13 +679,13 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False, dtype=None, str
     if residual is not None:
         _want("residual", residual, x.shape, (x.dtype, torch.float32), device)
     with _Call(device, stream, x, weight, residual) as raw:
-        # (empty_like takes half of empty's host time)
+        # (empty_like and new_empty take half and three quarters of empty's host time)
         h = None if residual is None else torch.empty_like(residual)
         y = None if quantize is True else torch.empty_like(x) if dtype is x.dtype else torch.empty_like(x, dtype=dtype)
         codes = scales = None
         if quantize:
             codes = torch.empty_like(x, dtype=torch.uint8)
-            scales = torch.empty((*x.shape[:-1], -(-hidden // 128)), dtype=torch.float32, device=device)
+            scales = x.new_empty((*x.shape[:-1], -(-hidden // 128)), dtype=torch.float32)
         # a stream as it stands goes in as the residual, which may have another type than y
         first, second = (x, residual) if residual is not None or x.dtype == dtype else (None, x)
         _mm._check(_mm.lib().mega_moe_rms_norm(
@@ -726,8 +726,8 @@ def rms_norm_backward(dy, h, weight, eps=1e-6, dresidual=None, stream=None):
     nbytes = _norm_bytes(rows, hidden)
     with _Call(device, stream, dy, values, scales, weight, dresidual) as raw:
         dx = torch.empty_like(dy) if kind is dy.dtype else torch.empty_like(dy, dtype=kind)
-        dweight = torch.empty(hidden, dtype=torch.float32, device=device)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        dweight = dy.new_empty(hidden, dtype=torch.float32)
+        workspace = dy.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
         _mm._check(_mm.lib().mega_moe_rms_norm_backward(
             dy.data_ptr(), values.data_ptr(), _at(scales), weight.data_ptr(), _at(dresidual), dx.data_ptr(), dweight.data_ptr(), rows,
             hidden, eps, kinds[dy.dtype], kinds[kind], kinds[weight.dtype], _at(workspace), nbytes, raw), "rms_norm_backward")
@@ -769,11 +769,11 @@ def swiglu(gate_up, checkpoint=False, offsets=None, status=None, stream=None):
     device = gate_up.device
     groups = _swiglu_groups(offsets, status, device)
     with _Call(device, stream, gate_up, offsets, status) as raw:
-        act = torch.empty((rows, inter), dtype=gate_up.dtype, device=device)
+        act = gate_up.new_empty((rows, inter))
         codes = scales = None
         if checkpoint:
             codes = torch.empty_like(gate_up, dtype=torch.uint8)
-            scales = torch.empty((rows, 2 * -(-inter // 128)), dtype=torch.float32, device=device)
+            scales = gate_up.new_empty((rows, 2 * -(-inter // 128)), dtype=torch.float32)
         _mm._check(_mm.lib().mega_moe_swiglu(gate_up.data_ptr(), act.data_ptr(), _at(codes), _at(scales), _at(offsets), groups,
                                              rows, inter, kinds[gate_up.dtype], _at(status), raw), "swiglu")
     act = _unrecorded("swiglu", "compute its gradient with swiglu_backward", act, gate_up)
@@ -799,7 +799,7 @@ def swiglu_backward(dact, gate_up, recompute=False, offsets=None, status=None, s
         _want("gate_up", gate_up, (rows, 2 * inter), (dact.dtype,), device)
     groups = _swiglu_groups(offsets, status, device)
     with _Call(device, stream, dact, values, scales, offsets, status) as raw:
-        dgate_up = torch.empty((rows, 2 * inter), dtype=dact.dtype, device=device)
+        dgate_up = dact.new_empty((rows, 2 * inter))
         act = torch.empty_like(dact) if recompute else None
         _mm._check(_mm.lib().mega_moe_swiglu_backward(
             dact.data_ptr(), values.data_ptr(), _at(scales), dgate_up.data_ptr(), _at(act), _at(offsets), groups, rows, inter,
