@@ -11,7 +11,7 @@
 // weights: 1024 x 7168 x 2048 over 32 groups 171 us (5.6 TB/s), eight rows for eight groups of 4096 x 7168 78 us (6.0).
 // The gradient of rows (8192 rows, 32 x 4096 x 1536: 148 us, 700 TFLOP/s, 3.3 TB/s) has the forward's bounds, and both
 // at once.  The gradient of weights of short groups writes as much as it multiplies, and the two share the CUs' time:
-// 16384 rows, 32 x 4096 x 7168, fp32, 1.39 ms for 962 GFLOP and 4.1 GB.
+// 16384 rows, 32 x 4096 x 7168, fp32, 1.38 ms for 962 GFLOP and 4.1 GB.
 #include <type_traits>
 
 #include "codes_loop.h"
@@ -316,7 +316,7 @@ hipError_t launch_weight_with(const GroupedArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// 256 x 256 tiles where they fill the CUs (16384 rows, 32 x 4096 x 7168, fp32: 1.39 ms as streams of tiles, 1.44 with a
+// 256 x 256 tiles where they fill the CUs (16384 rows, 32 x 4096 x 7168, fp32: 1.38 ms as streams of tiles, 1.44 with a
 // work-group for each, 1.75 with 128 x 128).  Below that the smaller ones, four times as many, and where these leave CUs without work and the
 // groups are long, the rows are split into parts of at least four steps (of an average group) that a second launch adds up.
 constexpr int kWeightLarge = 192;

@@ -6,7 +6,7 @@
 // is fp32 but the sums over a row, which are joined in fp64; y and the codes come from the unrounded sum v, each with its
 // one rounding.
 //
-// Bound by memory.  Measured, bf16, 32768 x 7168: x, residual, h, y and codes 360 us (2.12 GB, 5.9 TB/s); x and y 193 us
+// Bound by memory.  Measured, bf16, 32768 x 7168: x, residual, h, y and codes 362 us (2.12 GB, 5.9 TB/s); x and y 193 us
 // (4.9); the gradient with dresidual 354 us (1.88 GB, 5.3).  1024 x 7168 from an fp32 stream to codes: 17 us (4.8).  One row: 3.5 us,
 // of which the launch is most.
 #include <type_traits>
@@ -34,8 +34,8 @@ __device__ __forceinline__ void weights8(const void* w, int fp32, int c, int n, 
 
 // Sums over the lanes of a row.  kLanes 16 or 64: within the wave.  0: the whole work-group, through LDS that alternates
 // between two buffers from row to row, so that one barrier a row is enough: a buffer is written again only after the
-// barrier of the row in between.  A lane adds its few values in fp32 and the lanes are joined in fp64: r is then known to
-// half a step of fp32: its error is that of every value of the row, and moves some over the borders of the 8-bit grid.
+// barrier of the row in between.  A lane adds its few values and the lanes are joined in fp64: r's error is that of every
+// value of the row.
 template <int kLanes, int kSums>
 __device__ __forceinline__ void row_sums(double (&v)[kSums], double (*lds)[kSums], int turn) {
 #pragma unroll
@@ -98,7 +98,8 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
             x[u] = Row8<T>::load(a.x, at + c, a.x ? a.hidden - c : 0);
             res[u] = Row8<R>::load(a.residual, at + c, a.residual ? a.hidden - c : 0);
         }
-        float v[kUnits][8], squares = 0.f;
+        float v[kUnits][8];
+        typename std::conditional<kCodes, double, float>::type squares = 0;      // see below: codes ask for more of r
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int c = (u * p.lanes + p.lane) * 8;
@@ -108,7 +109,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 v[u][i] += r[i];
-                squares += v[u][i] * v[u][i];
+                squares += (decltype(squares))v[u][i] * v[u][i];
             }
             if (a.h) Row8<R>::store(a.h, at + c, a.hidden - c, v[u]);
         }
@@ -126,10 +127,10 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
                 for (int i = 0; i < 8; ++i) v[u][i] *= r * w[i];
                 if (a.y) Row8<T>::store(a.y, at + c, n, v[u]);
             } else {
-                // For the codes what the products lose is added to them: y is within half a step of fp32 of v r w, and what is
-                // left of it makes y odd, which the halves between two codes are not.  So the codes are those of v r w but
-                // for r's last bit and v's rounding: of 44 million values 4 fell on the other side of a half, 20 with fp32 products
-                // alone (32768 x 7168, y and codes: 360 us against 353).
+                // For the codes a lane adds its squares in fp64 too, and what the products lose is added to them: y is within
+                // half a step of fp32 of v r w, and what is left of it makes y odd, which the halves between two codes are
+                // not.  So the codes are those of v r w, whatever v is in fp32: of 88 million values of bf16 rows none fell on
+                // the other side of a half, 59 with fp32 throughout (32768 x 7168, y and codes: 362 us against 353).
                 float rest[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {

@@ -205,9 +205,9 @@ int32_t mega_moe_grouped_backward_weight_codes(const void* dy, const uint8_t* co
  *             both NULL; at least one of the three
  *   dtype     MEGA_MOE_BF16, _FP16 or _FP32; residual_dtype, weight_dtype: dtype or MEGA_MOE_FP32
  *   rows 0 .. MEGA_MOE_MAX_GROUP_ROWS (pointers may be NULL at 0), hidden 1 .. MEGA_MOE_MAX_NORM_COLS; eps >= 0, finite
- * v and the sums are fp32; y and the codes are computed from v, not from h, and rounded once each (beside codes, y is
- * computed to half a step of fp32 and may differ in its last bit from a call without them).  Squares beyond fp32's range
- * (values from 1.8e19 on) give y = 0.
+ * v is fp32; y and the codes are computed from v, not from h, and rounded once each.  Without codes the squares and products
+ * are fp32's (values from 1.8e19 on give y = 0); codes are those of the exact v w / sqrt(...), and y beside them is within
+ * half a step of fp32 of it before its rounding, so that it may differ in its last bit from a call without codes.
  * Errors: INVALID_ARG, UNSUPPORTED, HIP. */
 int32_t mega_moe_rms_norm(const void* x, const void* residual, const void* weight, void* h, void* y, uint8_t* codes, float* scales,
                           int64_t rows, int32_t hidden, float eps, int32_t dtype, int32_t residual_dtype, int32_t weight_dtype,
