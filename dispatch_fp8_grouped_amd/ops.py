@@ -337,6 +337,30 @@ class _Call:
             self.ctx.__exit__(*exc)
 
 
+class _Here:
+    """A call on the current stream of a device that is the current one already."""
+    __slots__ = ("index",)
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        return _current()[1](self.index)
+
+    def __exit__(self, *exc):
+        return None
+
+
+_HERE = [_Here(i) for i in range(128)]
+
+
+def _on(device, stream, *tensors):
+    """_Call(device, stream, *tensors); most calls need no more than the handle of the current stream, and no object for it."""
+    if stream is None and _current()[0]() == device.index:
+        return _HERE[device.index]
+    return _Call(device, stream, *tensors)
+
+
 _KINDS = {}
 
 
@@ -632,7 +656,7 @@ def quantize_rows(x, stream=None):
     holds an infinity or a NaN becomes NaN.  See mega_moe_ops.h."""
     import torch
     rows, cols = _rows("x", x)
-    with _Call(x.device, stream, x) as raw:
+    with _on(x.device, stream, x) as raw:
         codes = torch.empty_like(x, dtype=torch.uint8)
         scales = x.new_empty((*x.shape[:-1], -(-cols // 128)), dtype=torch.float32)
         _mm._check(_mm.lib().mega_moe_quantize_rows(x.data_ptr(), codes.data_ptr(), scales.data_ptr(), rows, cols,
@@ -651,7 +675,7 @@ def dequantize_rows(codes, scales, dtype=None, stream=None):
     cols = codes.shape[-1]
     if cols >> 31:
         _int32(cols=cols)
-    with _Call(codes.device, stream, codes, scales) as raw:
+    with _on(codes.device, stream, codes, scales) as raw:
         y = torch.empty_like(codes, dtype=dtype)
         _mm._check(_mm.lib().mega_moe_dequantize_rows(codes.data_ptr(), scales.data_ptr(), y.data_ptr(), codes.numel() // cols,
                                                       cols, kinds[dtype], raw), "dequantize_rows")
@@ -669,6 +693,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False, dtype=None, str
     import torch
     if quantize not in (False, True, "both"):
         raise ValueError(f'quantize: want False, True or "both", got {quantize!r}')
+    alone = bool(quantize) and quantize != "both"
     kinds = _logit_kinds()
     rows, hidden = _rows("x", x)
     device, given = x.device, x
@@ -678,10 +703,10 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False, dtype=None, str
     _want("weight", weight, (hidden,), (dtype, torch.float32), device)
     if residual is not None:
         _want("residual", residual, x.shape, (x.dtype, torch.float32), device)
-    with _Call(device, stream, x, weight, residual) as raw:
+    with _on(device, stream, x, weight, residual) as raw:
         # (empty_like and new_empty take half and three quarters of empty's host time)
         h = None if residual is None else torch.empty_like(residual)
-        y = None if quantize is True else torch.empty_like(x) if dtype is x.dtype else torch.empty_like(x, dtype=dtype)
+        y = None if alone else torch.empty_like(x) if dtype is x.dtype else torch.empty_like(x, dtype=dtype)
         codes = scales = None
         if quantize:
             codes = torch.empty_like(x, dtype=torch.uint8)
@@ -724,7 +749,7 @@ def rms_norm_backward(dy, h, weight, eps=1e-6, dresidual=None, stream=None):
     if dresidual is not None:
         _want("dresidual", dresidual, dy.shape, (kind,) if scales is None else (dy.dtype, torch.float32), device)
     nbytes = _norm_bytes(rows, hidden)
-    with _Call(device, stream, dy, values, scales, weight, dresidual) as raw:
+    with _on(device, stream, dy, values, scales, weight, dresidual) as raw:
         dx = torch.empty_like(dy) if kind is dy.dtype else torch.empty_like(dy, dtype=kind)
         dweight = dy.new_empty(hidden, dtype=torch.float32)
         workspace = dy.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
@@ -768,7 +793,7 @@ def swiglu(gate_up, checkpoint=False, offsets=None, status=None, stream=None):
     rows, inter = _swiglu_sizes("swiglu", gate_up, "gate_up", 2)
     device = gate_up.device
     groups = _swiglu_groups(offsets, status, device)
-    with _Call(device, stream, gate_up, offsets, status) as raw:
+    with _on(device, stream, gate_up, offsets, status) as raw:
         act = gate_up.new_empty((rows, inter))
         codes = scales = None
         if checkpoint:
@@ -798,7 +823,7 @@ def swiglu_backward(dact, gate_up, recompute=False, offsets=None, status=None, s
         values, scales = gate_up, None
         _want("gate_up", gate_up, (rows, 2 * inter), (dact.dtype,), device)
     groups = _swiglu_groups(offsets, status, device)
-    with _Call(device, stream, dact, values, scales, offsets, status) as raw:
+    with _on(device, stream, dact, values, scales, offsets, status) as raw:
         dgate_up = dact.new_empty((rows, 2 * inter))
         act = torch.empty_like(dact) if recompute else None
         _mm._check(_mm.lib().mega_moe_swiglu_backward(

@@ -370,3 +370,13 @@ def test_kept_values_cost_a_sixteenth():
         d = dy[s].double().abs().t().contiguous()
         bound = d @ half[s] + 2 * 301 * ref.U * (d @ (x[s].double().abs() + half[s]))
         assert ((a[e].double() - b[e].double()).abs() <= bound).all()
+
+
+def test_quantize_is_read_as_a_truth_value():
+    x, w = torch.randn(3, 128, device="cuda"), torch.ones(128, device="cuda")
+    for alone in (True, 1):
+        y, _, rows8 = mm.rms_norm(x, w, quantize=alone)
+        assert y is None and rows8 is not None
+    for none in (False, 0):
+        y, _, rows8 = mm.rms_norm(x, w, quantize=none)
+        assert y is not None and rows8 is None
