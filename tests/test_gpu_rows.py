@@ -482,3 +482,28 @@ def test_weight_gradient_takes_the_restored_values(kind, powers):
     fine = torch.isfinite(want).all(0)                 # beyond fp16's range an infinity meets dy's zeros in its column
     assert fine.all() or (kind == "fp16" and not powers and fine.sum() > 100)
     assert torch.equal(dw[0][:, fine], want.float()[:, fine])
+
+
+def test_weight_gradient_past_32_bits_of_codes():
+    """Rows whose codes lie beyond 2^32 bytes, in the last group."""
+    counts, n, k = [65530, 0, 4470], 8, 65536
+    rows = sum(counts)
+    codes = torch.empty(rows, k, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(rows, k // 128, device="cuda")
+    for at in range(0, rows, 8192):
+        s = slice(at, min(at + 8192, rows))
+        codes[s], scales[s] = mm.quantize_rows(normal((s.stop - at, k), BF16, at))
+    dy = normal((rows, n), BF16, 3)
+    off = [0, 65530, 65530, rows]
+    dw = mm.grouped_backward_weight(dy, (codes, scales), torch.tensor(off, dtype=torch.int32, device="cuda"), dtype=FP32)
+    assert (dw[1] == 0).all()
+    last = slice(off[2], rows)
+    check_weight(dy[last], ref.decode(codes[last], scales[last]), [0, counts[2]], dw[2:])
+    # the last columns of the first group, from all of its rows
+    part = mm.grouped_backward_weight(dy[:65530], (codes[:65530, -128:].contiguous(), scales[:65530, -1:].contiguous()),
+                                      torch.tensor([0, 65530], dtype=torch.int32, device="cuda"), dtype=FP32)
+    value = ref.decode(codes[:65530, -128:], scales[:65530, -1:])
+    check_weight(dy[:65530], value, [0, 65530], part)
+    check_weight(dy[:65530], value, [0, 65530], dw[:1, :, -128:])
+    del codes, scales
+    torch.cuda.empty_cache()
